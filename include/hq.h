@@ -434,6 +434,123 @@ HQ_API int hq_kv_read(const hq_kv_cache *cache, void *out, int out_dtype, int64_
 HQ_API int hq_kv_scores(const hq_kv_cache *cache, const void *d_q, int32_t group, float *d_scores, int64_t len,
                         int64_t scores_ld, void *cuda_stream);
 
+/* Attention of a few query tokens over a compressed K and a compressed V cache, without
+ * writing K or V to memory: the serving step that hq_kv_scores begins.  The decoder's output
+ * goes straight into the products; since the rotation is linear, the queries and the output
+ * are rotated instead of every cached token.
+ *
+ * A cached token t < len is visible to a query at position p iff
+ *     t <= p  and  (window == 0  or  t > p - window  or  t < sinks).
+ *   out[i, h] = sum_t softmax_t(scale * q[i, h] . K[h / group, t]) V[h / group, t]
+ * over the visible tokens t the cache holds (hq_kv_repack may have dropped some), K and V
+ * being the reconstructions of hq_kv_read before their rounding to bf16.  A row that sees
+ * nothing gives zeros.  Scores, maxima, sums and the output's sums are fp32; codes enter the
+ * products in fp16 (at most 2^-11 of their value off; codes up to 2048 without dither exact),
+ * weights in fp16 too, queries as two fp16. */
+typedef struct hq_attn_spec {
+    int64_t len;    /* cached tokens to use: positions [0, len), len <= tokens of both caches */
+    int64_t window; /* positions a query sees back, its own included; 0: all */
+    int64_t sinks;  /* first positions that stay visible whatever the window; >= 0 */
+    float scale;    /* of q . k (1 / sqrt(128) as a rule); finite */
+    int32_t n_q;    /* query tokens, 0..64 */
+    int32_t group;  /* query heads per KV head, 1..64 */
+    int32_t reserved; /* 0 */
+} hq_attn_spec;     /* 40 bytes */
+
+/* Device workspace of hq_kv_attention and hq_kv_tree_attention for caches of `heads` KV heads
+ * of any length (partial results of the splits of the tokens: at most about 16 MB for 8 heads).
+ * Host only. */
+HQ_API int hq_kv_attention_workspace_bytes(int32_t heads, const hq_attn_spec *spec, size_t *bytes);
+
+/* The queries are the last n_q cached tokens: query i is at position len - n_q + i (n_q <= len),
+ * append them to both caches first.
+ *   k, v      : caches of the same heads, lattice and dither whose appends (or repacked ranges)
+ *               cover the same tokens; alpha, seed, Rice parameters and rotation may differ.
+ *               HQ_EINVAL if their counters differ, HQ_EUNSUPPORTED for another lattice or
+ *               dither; an append of V that covers other tokens than K's counts as corrupt.
+ *   d_q       : device, bf16, 16-byte aligned: query token i, head h (of heads * group) at
+ *               d_q[i * q_ld_token + h * q_ld_head], 128 elements; strides % 8 == 0.
+ *   out       : device, 16-byte aligned, bf16 (out_dtype 0) or fp32 (1), laid out by its
+ *               strides (% 8 for bf16, % 4 for fp32, >= 128 between vectors).
+ *   d_lse     : device, fp32 [n_q, heads * group], or NULL: log of the sum of exp(score) over
+ *               the visible tokens (-infinity if none), to merge with attention over others.
+ *   workspace : >= hq_kv_attention_workspace_bytes, 16-byte aligned; its contents need no
+ *               initialisation; two calls that may run at once need one each.
+ * A corrupt chunk's tokens count as zero vectors, and HQ_ST_CORRUPT goes to its cache's d_stats.
+ * n_q 0 does nothing.  Asynchronous on cuda_stream; the counters and the spec are those at the
+ * call (or its capture). */
+HQ_API int hq_kv_attention(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *spec, const void *d_q,
+                           int64_t q_ld_token, int64_t q_ld_head, void *out, int out_dtype, int64_t out_ld_token,
+                           int64_t out_ld_head, float *d_lse, void *workspace, size_t ws_bytes, void *cuda_stream);
+
+/* The same for a tree of n_q drafted tokens that are not cached: their K and V are plain bf16.
+ *   d_kd, d_vd : device, bf16, 16-byte aligned: draft j's vector of KV head h at
+ *                [j * d_ld_token + h * d_ld_head], strides % 8 == 0.
+ *   d_mask     : device, uint64 [n_q]: bit j of d_mask[i] says that query i sees draft j (its
+ *                ancestors and itself); bits at or past n_q are ignored.
+ * Draft i is at position len - 1 + popcount(d_mask[i]), its depth in the tree past the cache;
+ * a draft outside the query's window (by the positions, as above), or later than the query,
+ * is not visible whatever the mask says.  What an invisible draft holds does not matter.
+ * Accepted drafts are appended with hq_kv_append. */
+HQ_API int hq_kv_tree_attention(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *spec, const void *d_q,
+                                int64_t q_ld_token, int64_t q_ld_head, const void *d_kd, const void *d_vd,
+                                int64_t d_ld_token, int64_t d_ld_head, const uint64_t *d_mask, void *out, int out_dtype,
+                                int64_t out_ld_token, int64_t out_ld_head, float *d_lse, void *workspace,
+                                size_t ws_bytes, void *cuda_stream);
+
+/* Copy ranges of a cache's tokens into another cache, whose contents they replace: a fork (one
+ * range, all tokens), a roll back (the first tokens), an eviction (the sinks and the last
+ * tokens) or a merge (a text appended token by token: a chunk per token costs space and
+ * decoder lanes, full chunks do not).  No symbol is decoded or changed: tokens keep their
+ * positions and reconstruct to the same values.
+ *   src, dst   : filled by hq_kv_init, of the same heads and params (lattice, rice_k,
+ *                rice_dk_last, seed, dither, rotation); dst with buffers of its own (HQ_EINVAL
+ *                if any overlaps).
+ *   h_ranges   : host, n_ranges pairs [begin, end) of positions, begin < end <= src->tokens,
+ *                ascending and not overlapping; 0..32 of them (0 empties dst).  Each becomes
+ *                one append of dst (a row of its table), so all of its tokens need to have
+ *                been appended with one alpha.
+ *   workspace  : device, >= hq_kv_repack_workspace_bytes(heads, ranges), 16-byte aligned.
+ * dst's tokens become the last range's end, so appends go on from there; hq_kv_read and
+ * hq_kv_scores leave the output of dropped positions untouched, and attention does not see
+ * them.  dst's stats are replaced: status, payload_bits and stream_words are the copy's,
+ * max_symbol and max_abs_code the source's, int8_overflow_count 0 (symbols are not looked at).
+ * HQ_ST_CAPACITY as for an append;
+ * HQ_ST_CORRUPT if a token is not in src, has another alpha than its range's first, or
+ * lies in a corrupt chunk (it is stored as zero symbols).  Asynchronous on cuda_stream. */
+HQ_API int hq_kv_repack_workspace_bytes(int32_t heads, const int64_t *h_ranges, int32_t n_ranges, size_t *bytes);
+HQ_API int hq_kv_repack(const hq_kv_cache *src, hq_kv_cache *dst, const int64_t *h_ranges, int32_t n_ranges,
+                        void *workspace, size_t ws_bytes, void *cuda_stream);
+
+/* Norms of queries and keys per head and their position rotation, in one pass: what a layer
+ * does between its projections and hq_kv_append / hq_kv_attention. */
+typedef struct hq_rope_spec {
+    int32_t rot_dim;     /* leading coordinates that turn: even, 0..128 */
+    int32_t interleaved; /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1) */
+    int32_t norm;        /* 1: RMS norm of each head vector first; 0: rotation only */
+    float eps;           /* of the norm, >= 0 */
+} hq_rope_spec;          /* 16 bytes */
+
+/* For each token t and each head of q and of k, the bf16 vector x of 128 gives
+ *   y = norm ? x / sqrt(mean x^2 + eps) * w : x,
+ *   pair i (a, b) of y -> (a cos f - b sin f, b cos f + a sin f),  f = pos[t] * inv_freq[i],
+ * in fp32 (the angle's fraction of a turn in fp64), rounded to bf16 once.
+ *   q, k      : device, bf16, 16-byte aligned; vector (t, h) at [t * ld_token + h * ld_head];
+ *               strides % 8 == 0.  heads_q or heads_k may be 0 (its pointers are not used).
+ *   d_wq, d_wk: device, bf16 [128], 16-byte aligned, or NULL (ones); not used without norm.
+ *   d_inv_freq: device, fp64 [rot_dim / 2]: radians per position (theta^(-2 i / rot_dim), or
+ *               any scaled form).
+ *   d_pos     : device, int64 [tokens], or NULL: pos[t] = pos0 + t.
+ *   q_out, k_out: device, bf16, 16-byte aligned, with strides of their own (% 8 == 0, >= 128
+ *               between vectors): keys as [heads, tokens, 128] go to hq_kv_append as they are.
+ *               Each may be its input itself (same pointer and strides).
+ * Asynchronous on cuda_stream; HQ_EINVAL for a bad pointer, stride or spec. */
+HQ_API int hq_qk_norm_rope(const void *q, int64_t q_ld_token, int64_t q_ld_head, int32_t heads_q, const void *k,
+                           int64_t k_ld_token, int64_t k_ld_head, int32_t heads_k, int64_t tokens,
+                           const hq_rope_spec *spec, const void *d_wq, const void *d_wk, const double *d_inv_freq,
+                           const int64_t *d_pos, int64_t pos0, void *q_out, int64_t qo_ld_token, int64_t qo_ld_head,
+                           void *k_out, int64_t ko_ld_token, int64_t ko_ld_head, void *cuda_stream);
+
 /* Draw a Haar-uniform rotation for hq_params.rotation: d_q (device, 16-byte
  * aligned, 128 x 128 fp32 row-major) = the orthogonal factor Q of G = Q R with R
  * upper triangular and positive on its diagonal, where G[i][j] is the standard

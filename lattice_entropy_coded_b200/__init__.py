@@ -61,10 +61,20 @@ class hq_calib_result(C.Structure):
                 ("status", C.c_uint32)]
 
 
+class hq_attn_spec(C.Structure):
+    _fields_ = [("len", C.c_int64), ("window", C.c_int64), ("sinks", C.c_int64), ("scale", C.c_float),
+                ("n_q", C.c_int32), ("group", C.c_int32), ("reserved", C.c_int32)]
+
+
+class hq_rope_spec(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("norm", C.c_int32), ("eps", C.c_float)]
+
+
 STATS_BYTES = 40
 assert C.sizeof(hq_calib_spec) == 48 and C.sizeof(hq_calib_result) == 24
 assert C.sizeof(hq_params) == 48 and C.sizeof(hq_stats) == STATS_BYTES and C.sizeof(hq_kv_append_row) == 32
 assert C.sizeof(hq_kv_cache) == 144
+assert C.sizeof(hq_attn_spec) == 40 and C.sizeof(hq_rope_spec) == 16
 
 # C entry points: name -> (restype, argtypes)
 EXPORTS = {
@@ -111,6 +121,21 @@ EXPORTS = {
     "hq_dequantize_batch": (C.c_int, [C.c_void_p, C.c_uint64, C.c_uint64, C.c_void_p, C.c_int64, C.c_int64,
                                       C.c_int64, C.POINTER(hq_params), C.c_void_p, C.c_int, C.c_int64, C.c_int64,
                                       C.c_void_p, C.c_void_p]),
+    "hq_kv_attention_workspace_bytes": (C.c_int, [C.c_int32, C.POINTER(hq_attn_spec), C.POINTER(C.c_size_t)]),
+    "hq_kv_attention": (C.c_int, [C.POINTER(hq_kv_cache), C.POINTER(hq_kv_cache), C.POINTER(hq_attn_spec), C.c_void_p,
+                                  C.c_int64, C.c_int64, C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_void_p,
+                                  C.c_void_p, C.c_size_t, C.c_void_p]),
+    "hq_kv_tree_attention": (C.c_int, [C.POINTER(hq_kv_cache), C.POINTER(hq_kv_cache), C.POINTER(hq_attn_spec),
+                                       C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64,
+                                       C.c_void_p, C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p,
+                                       C.c_size_t, C.c_void_p]),
+    "hq_kv_repack_workspace_bytes": (C.c_int, [C.c_int32, C.c_void_p, C.c_int32, C.POINTER(C.c_size_t)]),
+    "hq_kv_repack": (C.c_int, [C.POINTER(hq_kv_cache), C.POINTER(hq_kv_cache), C.c_void_p, C.c_int32, C.c_void_p,
+                               C.c_size_t, C.c_void_p]),
+    "hq_qk_norm_rope": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int32, C.c_void_p, C.c_int64, C.c_int64,
+                                  C.c_int32, C.c_int64, C.POINTER(hq_rope_spec), C.c_void_p, C.c_void_p, C.c_void_p,
+                                  C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_int64,
+                                  C.c_int64, C.c_void_p]),
 }
 
 
@@ -383,6 +408,103 @@ def hq_kv_read(cache: hq_kv_cache, out: torch.Tensor, length: int, cuda_stream=N
                                   _stream(cuda_stream)), "hq_kv_read")
 
 
+def attn_spec(length: int, scale: float, n_q: int, group: int, window: int = 0, sinks: int = 0) -> hq_attn_spec:
+    """What an attention call sees: cached positions [0, length), `window` back from each query (0: all)
+    and the first `sinks`; n_q query tokens, `group` query heads per KV head."""
+    return hq_attn_spec(int(length), int(window), int(sinks), float(scale), int(n_q), int(group), 0)
+
+
+def hq_kv_attention_workspace_bytes(heads: int, spec: hq_attn_spec) -> int:
+    b = C.c_size_t()
+    _check(_lib.hq_kv_attention_workspace_bytes(heads, C.byref(spec), C.byref(b)), "hq_kv_attention_workspace_bytes")
+    return int(b.value)
+
+
+def _attn_shapes(k: hq_kv_cache, spec: hq_attn_spec, q, out, lse) -> None:
+    shape = (spec.n_q, k.heads * spec.group, 128)
+    assert q.dtype == torch.bfloat16 and tuple(q.shape) == shape and q.stride(2) == 1
+    assert out.dtype in (torch.bfloat16, torch.float32) and tuple(out.shape) == shape and out.stride(2) == 1
+    assert lse is None or (lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == shape[:2])
+
+
+def hq_kv_attention(k: hq_kv_cache, v: hq_kv_cache, spec: hq_attn_spec, q: torch.Tensor, out: torch.Tensor,
+                    workspace: torch.Tensor, lse: torch.Tensor | None = None, cuda_stream=None) -> int:
+    """q bf16, out bf16 or fp32 [n_q, heads * group, 128] (unit stride in the last dimension): the queries
+    are the last n_q of spec.len cached tokens; lse: fp32 [n_q, heads * group] or None."""
+    _attn_shapes(k, spec, q, out, lse)
+    return _check(_lib.hq_kv_attention(C.byref(k), C.byref(v), C.byref(spec), _ptr(q), q.stride(0), q.stride(1),
+                                       _ptr(out), 1 if out.dtype == torch.float32 else 0, out.stride(0), out.stride(1),
+                                       _ptr(lse), _ptr(workspace), workspace.numel(), _stream(cuda_stream)),
+                  "hq_kv_attention")
+
+
+def hq_kv_tree_attention(k: hq_kv_cache, v: hq_kv_cache, spec: hq_attn_spec, q: torch.Tensor, kd: torch.Tensor,
+                         vd: torch.Tensor, mask: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
+                         lse: torch.Tensor | None = None, cuda_stream=None) -> int:
+    """As hq_kv_attention for n_q drafted tokens that are not cached: kd, vd bf16 [heads, n_q, 128] (equal
+    strides, the last 1); mask int64 [n_q], bit j of mask[i]: query i sees draft j."""
+    _attn_shapes(k, spec, q, out, lse)
+    assert kd.dtype == vd.dtype == torch.bfloat16 and kd.stride() == vd.stride() and kd.stride(2) == 1
+    assert tuple(kd.shape) == tuple(vd.shape) == (k.heads, spec.n_q, 128)
+    assert mask.dtype == torch.int64 and mask.is_contiguous() and mask.numel() == spec.n_q
+    return _check(_lib.hq_kv_tree_attention(C.byref(k), C.byref(v), C.byref(spec), _ptr(q), q.stride(0), q.stride(1),
+                                            _ptr(kd), _ptr(vd), kd.stride(1), kd.stride(0), _ptr(mask), _ptr(out),
+                                            1 if out.dtype == torch.float32 else 0, out.stride(0), out.stride(1),
+                                            _ptr(lse), _ptr(workspace), workspace.numel(), _stream(cuda_stream)),
+                  "hq_kv_tree_attention")
+
+
+def _ranges(ranges):
+    flat = [int(x) for r in ranges for x in r]
+    return (C.c_int64 * max(len(flat), 1))(*flat), len(flat) // 2
+
+
+def hq_kv_repack_workspace_bytes(heads: int, ranges) -> int:
+    r, n = _ranges(ranges)
+    b = C.c_size_t()
+    _check(_lib.hq_kv_repack_workspace_bytes(heads, r, n, C.byref(b)), "hq_kv_repack_workspace_bytes")
+    return int(b.value)
+
+
+def hq_kv_repack(src: hq_kv_cache, dst: hq_kv_cache, ranges, workspace: torch.Tensor | None, cuda_stream=None) -> int:
+    """dst's contents become the tokens of `ranges` (pairs [begin, end), ascending) of src."""
+    r, n = _ranges(ranges)
+    ws = 0 if workspace is None else workspace.numel()
+    return _check(_lib.hq_kv_repack(C.byref(src), C.byref(dst), r, n, _ptr(workspace), ws, _stream(cuda_stream)),
+                  "hq_kv_repack")
+
+
+def rope_spec(rot_dim: int = 128, interleaved: int = 0, norm: int = 1, eps: float = 1e-6) -> hq_rope_spec:
+    return hq_rope_spec(int(rot_dim), int(interleaved), int(norm), float(eps))
+
+
+def hq_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, spec: hq_rope_spec, inv_freq: torch.Tensor | None,
+                    q_out: torch.Tensor | None, k_out: torch.Tensor | None, wq: torch.Tensor | None = None,
+                    wk: torch.Tensor | None = None, positions: torch.Tensor | None = None, pos0: int = 0,
+                    cuda_stream=None) -> int:
+    """q, q_out bf16 [tokens, heads_q, 128]; k, k_out bf16 [heads_k, tokens, 128] (the layout hq_kv_append
+    takes); any strides, the last 1.  inv_freq fp64 [rot_dim / 2]; positions int64 [tokens] or None
+    (pos0 + t); wq, wk bf16 [128] or None."""
+    tokens = q.shape[0] if q is not None else k.shape[1] if k is not None else 0
+    for t, o, tok in ((q, q_out, 0), (k, k_out, 1)):
+        if t is None:
+            continue
+        assert t.dtype == o.dtype == torch.bfloat16 and t.shape == o.shape and t.dim() == 3
+        assert t.shape[2] == 128 and t.stride(2) == 1 and o.stride(2) == 1 and t.shape[tok] == tokens
+    assert spec.rot_dim == 0 or (inv_freq.dtype == torch.float64 and inv_freq.is_contiguous()
+                                 and inv_freq.numel() == spec.rot_dim // 2)
+    for w in (wq, wk):
+        assert w is None or (w.dtype == torch.bfloat16 and w.is_contiguous() and w.numel() == 128)
+    assert positions is None or (positions.dtype == torch.int64 and positions.is_contiguous()
+                                 and positions.numel() == tokens)
+    qs, qo = ((t.stride(0), t.stride(1)) if t is not None else (0, 0) for t in (q, q_out))
+    ks, ko = ((t.stride(1), t.stride(0)) if t is not None else (0, 0) for t in (k, k_out))
+    return _check(_lib.hq_qk_norm_rope(_ptr(q), *qs, q.shape[1] if q is not None else 0, _ptr(k), *ks,
+                                       k.shape[0] if k is not None else 0, tokens, C.byref(spec), _ptr(wq), _ptr(wk),
+                                       _ptr(inv_freq), _ptr(positions), int(pos0), _ptr(q_out), *qo, _ptr(k_out), *ko,
+                                       _stream(cuda_stream)), "hq_qk_norm_rope")
+
+
 # ------------------------------------------------------------------ torch-allocated wrappers
 def stats_tensor(device="cuda") -> torch.Tensor:
     return torch.zeros(STATS_BYTES, dtype=torch.uint8, device=device)
@@ -481,4 +603,44 @@ class KVCache:
                cuda_stream=None) -> torch.Tensor:
         """out[h * group + g, t] = K[h, t] . q[h * group + g] straight from the compressed cache."""
         hq_kv_scores(self.cache, q, group, out, self.tokens if length is None else length, cuda_stream)
+        return out
+
+    def repack(self, dst: "KVCache", ranges=None, cuda_stream=None) -> "KVCache":
+        """dst's contents become the tokens of `ranges` of this cache (default: all of them, one range), in
+        full chunks; dst: another KVCache of the same heads and params."""
+        ranges = ([(0, self.tokens)] if self.tokens else []) if ranges is None else ranges
+        ws = torch.empty(hq_kv_repack_workspace_bytes(self.heads, ranges), dtype=torch.uint8, device=dst.words.device)
+        hq_kv_repack(self.cache, dst.cache, ranges, ws, cuda_stream)
+        if cuda_stream is not None:   # torch may reuse the workspace's memory only after that stream is done with it
+            ws.record_stream(cuda_stream if isinstance(cuda_stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(int(cuda_stream)))
+        return dst
+
+
+class KVAttention:
+    """Attention over the K and V caches of one layer.  Owns the workspace, which serves calls that follow one
+    another (calls on several streams at once need an object each); its size covers every number of queries, so it
+    never moves under a captured graph."""
+
+    def __init__(self, k: KVCache, v: KVCache, group: int, scale: float = 128 ** -0.5, window: int = 0, sinks: int = 0):
+        self.k, self.v, self.group, self.scale, self.window, self.sinks = k, v, group, scale, window, sinks
+        need = max(hq_kv_attention_workspace_bytes(k.heads, attn_spec(0, scale, n, group)) for n in range(1, 65))
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=k.words.device)
+
+    def _spec(self, n_q: int, length: int | None) -> hq_attn_spec:
+        return attn_spec(self.k.tokens if length is None else length, self.scale, n_q, self.group, self.window,
+                         self.sinks)
+
+    def __call__(self, q: torch.Tensor, out: torch.Tensor, length: int | None = None, lse: torch.Tensor | None = None,
+                 cuda_stream=None) -> torch.Tensor:
+        """q, out [n_q, heads * group, 128]: the last n_q cached tokens' attention."""
+        spec = self._spec(q.shape[0], length)
+        hq_kv_attention(self.k.cache, self.v.cache, spec, q, out, self.workspace, lse, cuda_stream)
+        return out
+
+    def tree(self, q: torch.Tensor, kd: torch.Tensor, vd: torch.Tensor, mask: torch.Tensor, out: torch.Tensor,
+             length: int | None = None, lse: torch.Tensor | None = None, cuda_stream=None) -> torch.Tensor:
+        """The attention of n_q drafted tokens over the cache and one another (hq_kv_tree_attention)."""
+        spec = self._spec(q.shape[0], length)
+        hq_kv_tree_attention(self.k.cache, self.v.cache, spec, q, kd, vd, mask, out, self.workspace, lse, cuda_stream)
         return out

@@ -1,0 +1,286 @@
+// hq_attention.cu -- the entry points of attention over compressed KV caches, their argument
+// checks, and the kernel that joins the splits' partial results (hq_attention.cuh).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "hq_attention.cuh"
+
+namespace hq {
+
+namespace {
+
+constexpr int kCombineWarps = 8;
+
+// One warp per query row: the splits' sums rescaled to a common maximum and added, turned back
+// (D H_128, or Q^T), the visible drafts added, divided by the sum of all weights.
+__global__ void __launch_bounds__(kCombineWarps * 32) attention_combine(const __grid_constant__ AttnArgs a) {
+    __shared__ uint32_t sign[4];
+    __shared__ float xs[kCombineWarps][128];
+    __shared__ float ps[kCombineWarps][kAttnMaxQueries];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    build_sign_table(sign, 1, a.seed[1]);
+    __syncthreads();
+    const int row = blockIdx.x * kCombineWarps + warp, head = blockIdx.y;
+    if (row >= a.rows) return;
+    const int qi = row / a.group, qh = head * a.group + row - qi * a.group;
+
+    // drafts: log2 weights of two per lane
+    float m = kNegInf, sd[2] = {kNegInf, kNegInf};
+    unsigned long long mine = 0;
+    if (a.mask) {
+        const unsigned long long all = a.n_q < 64 ? (1ull << a.n_q) - 1ull : ~0ull;
+        mine = a.mask[qi] & all;
+        const int64_t pos = a.len - 1 + __popcll(mine);
+        const uint2 qr = *reinterpret_cast<const uint2 *>(a.q + qi * a.q_ld_tok + qh * a.q_ld_head + 4 * lane);
+        const float q[4] = {__uint_as_float(qr.x << 16), __uint_as_float(qr.x & 0xFFFF0000u),
+                            __uint_as_float(qr.y << 16), __uint_as_float(qr.y & 0xFFFF0000u)};
+        for (int j = 0; j < a.n_q; j++) {
+            float s = 0.0f;
+            if ((mine >> j) & 1ull) {
+                const uint2 kr = *reinterpret_cast<const uint2 *>(a.kd + j * a.d_ld_tok + head * a.d_ld_head + 4 * lane);
+                s = __fmul_rn(q[0], __uint_as_float(kr.x << 16));
+                s = __fmaf_rn(q[1], __uint_as_float(kr.x & 0xFFFF0000u), s);
+                s = __fmaf_rn(q[2], __uint_as_float(kr.y << 16), s);
+                s = __fmaf_rn(q[3], __uint_as_float(kr.y & 0xFFFF0000u), s);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+                const int64_t t = a.len - 1 + __popcll(a.mask[j] & all);
+                // a draft later than the query, or outside its window, is not visible whatever the mask says
+                const bool see = t <= pos && (a.window <= 0 || t > pos - a.window || t < a.sinks);
+                if ((j & 31) == lane) sd[j >> 5] = see ? __fmul_rn(s, a.scale_log2) : kNegInf;
+            }
+        }
+        m = fmaxf(sd[0], sd[1]);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
+    // splits
+    const int64_t step = (int64_t)a.heads * a.row_pad, at = (int64_t)head * a.row_pad + row;
+    float top = kNegInf;
+    for (int sp = lane; sp < a.splits; sp += 32) top = fmaxf(top, a.ml[sp * step + at].x);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    m = fmaxf(m, top);
+    const float base = m == kNegInf ? 0.0f : m;
+    float l = 0.0f, o4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int sp = 0; sp < a.splits; sp++) {
+        const float2 ml = a.ml[sp * step + at];
+        if (ml.y == 0.0f) continue;   // the split saw nothing of this row
+        const float f = ex2(__fsub_rn(ml.x, base));
+        const float4 x = *reinterpret_cast<const float4 *>(a.part + (sp * step + at) * kTile + 4 * lane);
+        l = __fmaf_rn(ml.y, f, l);
+        o4[0] = __fmaf_rn(x.x, f, o4[0]);
+        o4[1] = __fmaf_rn(x.y, f, o4[1]);
+        o4[2] = __fmaf_rn(x.z, f, o4[2]);
+        o4[3] = __fmaf_rn(x.w, f, o4[3]);
+    }
+    // back from the rotated domain
+    if (a.rot[1]) {
+        reinterpret_cast<float4 *>(xs[warp])[lane] = make_float4(o4[0], o4[1], o4[2], o4[3]);
+        __syncwarp();
+        o4[0] = o4[1] = o4[2] = o4[3] = 0.0f;
+        for (int i = 0; i < 128; i++) {
+            const float z = xs[warp][i];
+            const float4 q = __ldg(reinterpret_cast<const float4 *>(a.rot[1] + i * 128) + lane);
+            o4[0] = __fmaf_rn(q.x, z, o4[0]);
+            o4[1] = __fmaf_rn(q.y, z, o4[1]);
+            o4[2] = __fmaf_rn(q.z, z, o4[2]);
+            o4[3] = __fmaf_rn(q.w, z, o4[3]);
+        }
+    } else {
+        fwht_row(o4, lane);
+        const uint32_t e = sign[lane >> 3];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int c = (4 * lane + i) & 31;
+            if ((e >> ((c >> 1) + 16 * (c & 1))) & 1u) o4[i] = -o4[i];
+        }
+    }
+    if (mine) {
+        const float p0 = ex2(__fsub_rn(sd[0], base)), p1 = ex2(__fsub_rn(sd[1], base));
+        ps[warp][lane] = p0;
+        ps[warp][lane + 32] = p1;
+        float pl = __fadd_rn(p0, p1);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) pl = __fadd_rn(pl, __shfl_xor_sync(0xffffffffu, pl, o));
+        l = __fadd_rn(l, pl);
+        __syncwarp();
+        for (int j = 0; j < a.n_q; j++) {
+            const float p = ps[warp][j];
+            // a draft that the row does not see may hold anything
+            if (p == 0.0f) continue;
+            const uint2 vr = *reinterpret_cast<const uint2 *>(a.vd + j * a.d_ld_tok + head * a.d_ld_head + 4 * lane);
+            o4[0] = __fmaf_rn(p, __uint_as_float(vr.x << 16), o4[0]);
+            o4[1] = __fmaf_rn(p, __uint_as_float(vr.x & 0xFFFF0000u), o4[1]);
+            o4[2] = __fmaf_rn(p, __uint_as_float(vr.y << 16), o4[2]);
+            o4[3] = __fmaf_rn(p, __uint_as_float(vr.y & 0xFFFF0000u), o4[3]);
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);   // a row that sees nothing: zeros
+#pragma unroll
+    for (int i = 0; i < 4; i++) o4[i] = __fmul_rn(o4[i], inv);
+    const int64_t off = qi * a.out_ld_tok + qh * a.out_ld_head + 4 * lane;
+    if (a.out_fp32) {
+        *reinterpret_cast<float4 *>((float *)a.out + off) = make_float4(o4[0], o4[1], o4[2], o4[3]);
+    } else {
+        __nv_bfloat162 b0 = __floats2bfloat162_rn(o4[0], o4[1]), b1 = __floats2bfloat162_rn(o4[2], o4[3]);
+        *reinterpret_cast<uint2 *>((uint16_t *)a.out + off) =
+            make_uint2(*reinterpret_cast<uint32_t *>(&b0), *reinterpret_cast<uint32_t *>(&b1));
+    }
+    if (a.lse && lane == 0)
+        a.lse[(int64_t)qi * a.heads * a.group + qh] =
+            l == 0.0f ? kNegInf : __fmul_rn(__fadd_rn(m, log2f(l)), 0.69314718055994530942f);
+}
+
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+int check_spec(const hq_attn_spec *sp) {
+    if (!sp || sp->len < 0 || sp->window < 0 || sp->sinks < 0 || !isfinite(sp->scale)) return HQ_EINVAL;
+    if (sp->n_q < 0 || sp->group < 1) return HQ_EINVAL;
+    if (sp->n_q > kAttnMaxQueries || sp->group > kAttnMaxGroup || sp->len > (INT64_C(1) << 40)) return HQ_EUNSUPPORTED;
+    return HQ_OK;
+}
+
+int row_pad_of(int rows) {
+    const int rb = attn_row_block(rows);
+    return (rows + rb - 1) / rb * rb;
+}
+
+int attend(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *sp, const void *d_q, int64_t q_ld_token,
+           int64_t q_ld_head, bool tree, const void *d_kd, const void *d_vd, int64_t d_ld_token, int64_t d_ld_head,
+           const uint64_t *d_mask, void *out, int out_dtype, int64_t out_ld_token, int64_t out_ld_head, float *d_lse,
+           void *workspace, size_t ws_bytes, void *cuda_stream) {
+    int rc = check_spec(sp);
+    if (rc) return rc;
+    if (!k || !v || k == v || !k->d_words || !v->d_words || k->heads <= 0 || k->heads != v->heads) return HQ_EINVAL;
+    if (k->head_dim != kTile || v->head_dim != kTile) return HQ_EUNSUPPORTED;
+    if (out_dtype != 0 && out_dtype != 1) return HQ_EINVAL;
+    // the two caches' appends have to cover the same tokens (the device tables are compared too)
+    if (sp->len > k->tokens || sp->len > v->tokens || k->chunks != v->chunks || k->appends != v->appends) return HQ_EINVAL;
+    if (k->params.lattice != v->params.lattice || k->params.dither != v->params.dither) return HQ_EUNSUPPORTED;
+    if (!tree && sp->n_q > sp->len) return HQ_EINVAL;   // the queries are the last cached tokens
+    if (k->heads > 65535) return HQ_EUNSUPPORTED;       // a grid dimension
+    if (sp->n_q == 0) return HQ_OK;
+    const int m = out_dtype ? 4 : 8, n_heads = k->heads * sp->group;
+    if (!d_q || !aligned(d_q, 16) || q_ld_token < 0 || q_ld_token % 8 || q_ld_head < 0 || q_ld_head % 8) return HQ_EINVAL;
+    if (!out || !aligned(out, 16) || out_ld_token < 0 || out_ld_token % m || out_ld_head < 0 || out_ld_head % m)
+        return HQ_EINVAL;
+    // no two rows of the output share an element
+    if ((n_heads > 1 && out_ld_head < kTile) || (sp->n_q > 1 && out_ld_token < kTile)) return HQ_EINVAL;
+    if (d_lse && !aligned(d_lse, 4)) return HQ_EINVAL;
+    if (tree && (!d_kd || !aligned(d_kd, 16) || !d_vd || !aligned(d_vd, 16) || d_ld_token < 0 || d_ld_token % 8 ||
+                 d_ld_head < 0 || d_ld_head % 8 || !d_mask || !aligned(d_mask, 8)))
+        return HQ_EINVAL;
+    size_t need = 0;
+    if ((rc = hq_kv_attention_workspace_bytes(k->heads, sp, &need))) return rc;
+    if (!workspace || !aligned(workspace, 16) || ws_bytes < need) return HQ_EINVAL;
+    AttnArgs a;
+    memset(&a, 0, sizeof(a));
+    const hq_kv_cache *c[2] = {k, v};
+    for (int i = 0; i < 2; i++) {
+        a.words[i] = c[i]->d_words;
+        a.cap[i] = c[i]->cap_words;
+        a.offsets[i] = c[i]->d_offsets;
+        a.table[i] = c[i]->d_table;
+        a.stats[i] = c[i]->d_stats;
+        a.seed[i] = c[i]->params.seed;
+        a.rot[i] = c[i]->params.rotation;
+        a.k[i] = c[i]->params.rice_k;
+        a.k_last[i] = k_last_of(c[i]->params);
+    }
+    a.n_chunks = k->chunks;
+    a.n_appends = k->appends;
+    a.len = sp->len;
+    a.window = sp->window > sp->len + kAttnMaxQueries ? 0 : sp->window;   // sees everything
+    a.sinks = sp->sinks > sp->len + kAttnMaxQueries ? sp->len + kAttnMaxQueries : sp->sinks;
+    a.heads = k->heads;
+    a.group = sp->group;
+    a.n_q = sp->n_q;
+    a.rows = sp->n_q * sp->group;
+    a.row_pad = row_pad_of(a.rows);
+    a.scale = sp->scale;
+    a.scale_log2 = (float)((double)sp->scale * 1.4426950408889634074);
+    a.q = (const uint16_t *)d_q;
+    a.q_ld_tok = q_ld_token;
+    a.q_ld_head = q_ld_head;
+    if (tree) {
+        a.mask = (const unsigned long long *)d_mask;
+        a.kd = (const uint16_t *)d_kd;
+        a.vd = (const uint16_t *)d_vd;
+        a.d_ld_tok = d_ld_token;
+        a.d_ld_head = d_ld_head;
+    }
+    a.out = out;
+    a.out_fp32 = out_dtype;
+    a.out_ld_tok = out_ld_token;
+    a.out_ld_head = out_ld_head;
+    a.lse = d_lse;
+    cudaStream_t s = (cudaStream_t)cuda_stream;
+    const bool cached = sp->len > 0 && k->chunks > 0;
+    if (cached) {
+        // chunks a head's queries may see, as far as the host knows: all, or those of the window and the sinks
+        // (one more at each end of either)
+        uint64_t per_head = k->chunks / (uint64_t)k->heads;
+        if (a.window > 0) {
+            const uint64_t w = (uint64_t)(a.window + sp->n_q + a.sinks) + 4;
+            if (w < per_head) per_head = w;
+        }
+        a.splits = attn_splits(a.heads, a.rows, per_head);
+        a.part = (float *)workspace;
+        a.ml = (float2 *)(a.part + (size_t)a.splits * a.heads * a.row_pad * kTile);
+        if (launch_attention(k->params.lattice, k->params.dither, a, s) != cudaSuccess) return HQ_ECUDA;
+    }
+    const dim3 g((unsigned)((a.rows + kCombineWarps - 1) / kCombineWarps), (unsigned)a.heads);
+    attention_combine<<<g, kCombineWarps * 32, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? HQ_OK : HQ_ECUDA;
+}
+
+}  // namespace
+
+cudaError_t launch_attention(int lattice, int dither, const AttnArgs &a, cudaStream_t s) {
+    switch (lattice) {
+    case HQ_Z: return launch_attention_z(dither, a, s);
+    case HQ_A2: return launch_attention_a2(dither, a, s);
+    case HQ_D4: return launch_attention_d4(dither, a, s);
+    case HQ_E8: return launch_attention_e8(dither, a, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace hq
+
+using namespace hq;
+
+extern "C" {
+
+int hq_kv_attention_workspace_bytes(int32_t heads, const hq_attn_spec *spec, size_t *bytes) {
+    const int rc = check_spec(spec);
+    if (rc) return rc;
+    if (!bytes || heads <= 0) return HQ_EINVAL;
+    const int rows = spec->n_q * spec->group;
+    // as many splits as any cache of this many heads may take
+    const size_t splits = (size_t)attn_splits(heads, rows, UINT64_C(1) << 40);
+    *bytes = (splits * (size_t)heads * (size_t)row_pad_of(rows) * (kTile * sizeof(float) + sizeof(float2)) + 255) &
+             ~(size_t)255;
+    return HQ_OK;
+}
+
+int hq_kv_attention(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *spec, const void *d_q,
+                    int64_t q_ld_token, int64_t q_ld_head, void *out, int out_dtype, int64_t out_ld_token,
+                    int64_t out_ld_head, float *d_lse, void *workspace, size_t ws_bytes, void *cuda_stream) {
+    return attend(k, v, spec, d_q, q_ld_token, q_ld_head, false, nullptr, nullptr, 0, 0, nullptr, out, out_dtype,
+                  out_ld_token, out_ld_head, d_lse, workspace, ws_bytes, cuda_stream);
+}
+
+int hq_kv_tree_attention(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *spec, const void *d_q,
+                         int64_t q_ld_token, int64_t q_ld_head, const void *d_kd, const void *d_vd, int64_t d_ld_token,
+                         int64_t d_ld_head, const uint64_t *d_mask, void *out, int out_dtype, int64_t out_ld_token,
+                         int64_t out_ld_head, float *d_lse, void *workspace, size_t ws_bytes, void *cuda_stream) {
+    return attend(k, v, spec, d_q, q_ld_token, q_ld_head, true, d_kd, d_vd, d_ld_token, d_ld_head, d_mask, out,
+                  out_dtype, out_ld_token, out_ld_head, d_lse, workspace, ws_bytes, cuda_stream);
+}
+
+}  // extern "C"
