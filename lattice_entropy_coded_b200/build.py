@@ -38,7 +38,9 @@ NVCC_FLAGS = [
 def _stale(obj: str, src: str) -> bool:
     if not os.path.exists(obj):
         return True
-    deps = [src, os.path.join(INCLUDE, "hq.h")] + [os.path.join(CSRC, h) for h in HEADERS]
+    own = os.path.basename(src).startswith("hq_attention")   # the only sources that include hq_attention.cuh
+    deps = [src, os.path.join(INCLUDE, "hq.h")] + [os.path.join(CSRC, h) for h in HEADERS
+                                                   if own or h != "hq_attention.cuh"]
     t = os.path.getmtime(obj)
     return any(os.path.getmtime(d) > t for d in deps)
 

@@ -170,12 +170,120 @@ struct Piece {
     uint64_t chunk;       // chunk index (K's and V's)
 };
 
+// ------------------------------------------------------------------ E8 dither
+// d = w - Q(w) of dither_block<HQ_E8>, bit for bit, for an eighth of its work.  With w uniform on
+// [0, 4)^8, let c_i = (w_i mod 2) - 1 and b_i = |c_i|: c_i is w_i's residual to the nearest odd
+// integer (candidate B), and c_i - sign(c_i), of size 1 - b_i, the one to the nearest even integer
+// (candidate A).  The squared distances' difference is then linear in the b_i:
+//   (|w - A|^2 - |w - B|^2) / 2 = 4 - sum b + 2 p_A min b - 2 p_B (1 - max b),
+// the last terms being the parity fixes (the largest residual r becomes 2 - r), with the parities
+// of the rounded halves from the two top bits of each w: p_B the XOR of the "w >= 2", p_A of the
+// "1 <= w < 3".  So one pass over c serves both candidates.  Everything is exact in units of 2^-22
+// but the sum (within 16 units).  The reading compares fp32 distances, which are off by less than
+// 2^-16 here (the bound at Lattice<HQ_E8>): a difference within 2^-12, a coordinate on a rounding
+// border (b = 0 or 1) or two equal largest residuals under a fix goes to the reading's own code
+// instead, about one block in 4000.
+constexpr float kDitherUnit = 4194304.0f;       // 2^22: d is returned in units of 2^-22
+constexpr uint64_t kSplitGolden = 0x9E3779B97F4A7C15ull;
+
+// Two hashes' worth of a pair: generator state z (s + (i + 1) golden) -> w of the even and the odd
+// coordinate as 32-bit fixed point (bits 8..31 of each count).
+__device__ __forceinline__ void dither_pair(uint64_t z, uint32_t &even, uint32_t &odd) {
+    z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+    z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+    // h = z ^ (z >> 31): bits 40..63 are z's own, bits 8..31 take z's bits 39..62
+    even = (uint32_t)(z >> 32);
+    odd = (uint32_t)z ^ (even << 1);
+}
+
+__device__ __noinline__ void e8_dither_reading(const uint32_t *x, float *d) {
+    float w[8], p[8];
+    int32_t q[8];
+    for (int i = 0; i < 8; i++) w[i] = __fmul_rn((float)(x[i] >> 8), 0x1p-22f);
+    Lattice<HQ_E8>::nearest(w, q);
+    Lattice<HQ_E8>::point(q, p);
+    for (int i = 0; i < 8; i++) d[i] = __fmul_rn(__fsub_rn(w[i], p[i]), kDitherUnit);
+}
+
+// The block whose first pair has generator state z0; d in units of 2^-22.
+__device__ __forceinline__ void e8_dither(uint64_t z0, float (&d)[8]) {
+    uint32_t x[8];
+    float c[8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) dither_pair(z0 + (uint64_t)i * kSplitGolden, x[2 * i], x[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        // 2^23 + (w mod 2), less 2^23 + 1 (units of 2^-22): exact
+        const float2 f = make_float2(__uint_as_float(((x[2 * i] >> 8) & 0x7FFFFFu) | 0x4B000000u),
+                                     __uint_as_float(((x[2 * i + 1] >> 8) & 0x7FFFFFu) | 0x4B000000u));
+        const float2 r = f2_sub(f, make_float2(8388608.0f + kDitherUnit, 8388608.0f + kDitherUnit));
+        c[2 * i] = r.x;
+        c[2 * i + 1] = r.y;
+    }
+    const uint32_t par = (x[0] ^ x[1] ^ x[2]) ^ (x[3] ^ x[4] ^ x[5]) ^ (x[6] ^ x[7]);
+    const bool pb = (int32_t)par < 0, pa = (int32_t)(par ^ (par << 1)) < 0;
+    float lo = fabsf(c[0]), hi = lo;
+#pragma unroll
+    for (int i = 1; i < 8; i++) {
+        lo = fminf(lo, fabsf(c[i]));
+        hi = fmaxf(hi, fabsf(c[i]));
+    }
+    const float s0 = __fadd_rn(__fadd_rn(fabsf(c[0]), fabsf(c[1])), __fadd_rn(fabsf(c[2]), fabsf(c[3])));
+    const float s1 = __fadd_rn(__fadd_rn(fabsf(c[4]), fabsf(c[5])), __fadd_rn(fabsf(c[6]), fabsf(c[7])));
+    const float half = __fsub_rn(__fsub_rn(4.0f * kDitherUnit, s0), s1);
+    const float diff = __fadd_rn(half, __fsub_rn(pa ? __fadd_rn(lo, lo) : 0.0f,
+                                                 pb ? __fmul_rn(2.0f, __fsub_rn(kDitherUnit, hi)) : 0.0f));
+    const bool odd = diff > 0.0f, fix = odd ? pb : pa;
+    // d = c - sign(c) m: m = 0 (B) or 1 (A), and for the coordinate of the fix 2 (B) or -1 (A)
+    const float m0 = odd ? 0.0f : kDitherUnit, m1 = odd ? 2.0f * kDitherUnit : -kDitherUnit;
+    const float at = fix ? (odd ? hi : lo) : -1.0f;
+    float m[8];
+    float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 8; i++) m[i] = fabsf(c[i]) == at ? m1 : m0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        sum = f2_add(sum, make_float2(m[2 * i], m[2 * i + 1]));
+        const float2 r = f2_sub(make_float2(c[2 * i], c[2 * i + 1]),
+                                make_float2(__uint_as_float(__float_as_uint(m[2 * i]) ^ (__float_as_uint(c[2 * i]) & 0x80000000u)),
+                                            __uint_as_float(__float_as_uint(m[2 * i + 1]) ^
+                                                            (__float_as_uint(c[2 * i + 1]) & 0x80000000u))));
+        d[2 * i] = r.x;
+        d[2 * i + 1] = r.y;
+    }
+    const float want = fix ? __fadd_rn(__fmul_rn(7.0f, m0), m1) : __fmul_rn(8.0f, m0);
+    if (fabsf(diff) <= 1024.0f || lo == 0.0f || hi == kDitherUnit || __fadd_rn(sum.x, sum.y) != want) {
+        float t[8];
+        e8_dither_reading(x, t);
+#pragma unroll
+        for (int i = 0; i < 8; i++) d[i] = t[i];
+    }
+}
+
 // ------------------------------------------------------------------ decode
+// Forms of the Rice code: no remainders at all (k = 0: the 2-bit caches), remainders read four
+// windows at a time (k <= 4, one parameter), or bit by bit.
+enum AttnForm { kFormUnary = 0, kFormWindows = 1, kFormGeneral = 2 };
+
+// Unary pairs of E8 at k = 0: the next 10 stream bits -> both codewords.  Bits 0..4 their length,
+// byte 1 and byte 2 the two codes 2 m + 128 (2 m the zigzag inverse doubled), bit 24 the parity of
+// m of both, bit 25 of the first, bit 31 set if both codewords end inside the 10 bits (one pair in
+// 2000 does not at 2 bits per scalar).
+constexpr int kPairBits = 10;
+__device__ __forceinline__ uint32_t pair_entry(uint32_t w) {
+    const uint32_t t0 = (uint32_t)__ffs((int)(w | 0x80000000u)) - 1u;
+    const uint32_t t1 = t0 < 31u ? (uint32_t)__ffs((int)((w >> (t0 + 1u)) | 0x80000000u)) - 1u : 31u;
+    if (t0 + t1 + 2u > (uint32_t)kPairBits) return 0u;
+    const uint32_t a = t0 ^ (0u - (t0 & 1u)), b = t1 ^ (0u - (t1 & 1u));   // 2 m
+    return 0x80000000u | (t0 + t1 + 2u) | ((a + 128u) & 0xFFu) << 8 | ((b + 128u) & 0xFFu) << 16 |
+           (((a ^ b) >> 1) & 1u) << 24 | ((a >> 1) & 1u) << 25;
+}
+
 // The 32 codes (minus dither) of a lane's quarter of a tile, times `scale`, as 16 fp16 pairs.
-template <int LAT, bool DITHER, bool GENERAL, bool STAGED>
+template <int LAT, bool DITHER, int FORM, bool STAGED>
 __device__ __forceinline__ bool decode_quarter(const uint32_t *src, uint32_t nc, uint32_t nr, uint32_t nu, int k, int kl,
                                                uint32_t bp, uint32_t segi, int q, unsigned long long e0, uint64_t seed,
-                                               float scale, uint32_t (&w)[16]) {
+                                               float scale, const uint32_t *pairs, uint32_t (&w)[16]) {
     using L = Lattice<LAT>;
     constexpr int N = L::N;
     const uint32_t *un = src + nc + nr;
@@ -183,57 +291,111 @@ __device__ __forceinline__ bool decode_quarter(const uint32_t *src, uint32_t nc,
     const uint32_t gbits = group_rem_bits<N>(k, kl), lane_bits = 4u * gbits;
     bool ok = true;
     uint32_t rx[4] = {0u, 0u, 0u, 0u};
-    if (!GENERAL && k > 0) rem_windows(src + nc + segi * (uint32_t)k, k, rx);
+    if (FORM == kFormWindows && k > 0) rem_windows(src + nc + segi * (uint32_t)k, k, rx);
     const uint32_t cw = (LAT == HQ_E8) ? src[segi >> 3] : 0u;
     const uint32_t coset = (cw >> (4 * (segi & 7u))) & 0xFu;
     const float2 s2 = make_float2(scale, scale);
+    // E8 with dither: d comes in units of 2^-22
+    const float2 sd2 = make_float2(__fmul_rn(scale, -0x1p-22f), __fmul_rn(scale, -0x1p-22f));
+    const uint64_t z0 = (seed ^ kDitherSalt) + ((e0 >> 1) + (uint64_t)(16 * q) + 1ull) * kSplitGolden;
 #pragma unroll
     for (int g = 0; g < 4; g++) {
-        uint32_t qv[8], rv[8];
-        unary4<STAGED>(un, nu, bp, ok, qv);
-        unary4<STAGED>(un, nu, bp, ok, qv + 4);
-        if (GENERAL) {
-            rem_group_mixed<N, STAGED>(src + nc, nr, segi * lane_bits, g, k, kl, gbits, rv);
-        } else {
-            const uint32_t mask = (1u << k) - 1u;
-            uint32_t xw = rx[g];
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                rv[i] = xw & mask;
-                xw >>= k;
-            }
-        }
         float u[8];
+        if constexpr (LAT == HQ_E8 && FORM == kFormUnary && STAGED) {
+            // The plane's terminators were counted, so a lane's 32 codewords end inside it (or in the pad
+            // behind its last word, which the second word of a window may reach).
+            const uint32_t c = (coset >> g) & 1u;
+            uint32_t e[4], used = 0;
 #pragma unroll
-        for (int bb = 0; bb < 8 / N; bb++) {
-            int32_t qq[N];
-            float p[N];
-            if constexpr (LAT == HQ_E8) {
-                uint32_t zb[8];
+            for (int h = 0; h < 2; h++) {
+                const uint32_t *p = un + ((bp + used) >> 5);
+                uint32_t x = __funnelshift_r(p[0], p[1], bp + used);
+                e[2 * h] = pairs[x & ((1u << kPairBits) - 1u)];
+                x = __funnelshift_r(x, 0u, e[2 * h]);
+                e[2 * h + 1] = pairs[x & ((1u << kPairBits) - 1u)];
+                used += (e[2 * h] + e[2 * h + 1]) & 0x1Fu;
+            }
+            if ((int32_t)(e[0] & e[1] & e[2] & e[3]) < 0) {
+                bp += used;
+                // the stripped parity of m_7: that of m_0 .. m_6
+                const uint32_t p7 = ((e[0] ^ e[1] ^ e[2]) >> 24 ^ e[3] >> 25) & 1u;
+                const float off = __fsub_rn((float)(int)c, 8388608.0f + 128.0f);
+                const float2 o2 = make_float2(off, off);
 #pragma unroll
-                for (int i = 0; i < 8; i++) zb[i] = imad(qv[bb * N + i], i == N - 1 ? pkl : pk, rv[bb * N + i]);
-                e8_codes_from_symbols(zb, (coset >> g) & 1u, qq);
+                for (int h = 0; h < 4; h++) {
+                    const float2 f = make_float2(__uint_as_float(__byte_perm(e[h], 0x4B000000u, 0x7441)),
+                                                 __uint_as_float(__byte_perm(e[h], 0x4B000000u, 0x7442)));
+                    const float2 r = f2_add(f, o2);
+                    u[2 * h] = r.x;
+                    u[2 * h + 1] = r.y;
+                }
+                // 2 (2 m_7 + p) + c from 2 m_7 + c
+                u[7] = __fadd_rn(__fadd_rn(u[7], u[7]), (float)((int)(2u * p7) - (int)c));
             } else {
-                int32_t m[N];
+                uint32_t zq[8];
+                unary4<STAGED>(un, nu, bp, ok, zq);
+                unary4<STAGED>(un, nu, bp, ok, zq + 4);
+                int32_t qq[8];
+                e8_codes_from_symbols(zq, c, qq);
+                decoded_point<HQ_E8>(qq, u);
+            }
+        } else {
+            uint32_t qv[8], rv[8];
+            unary4<STAGED>(un, nu, bp, ok, qv);
+            unary4<STAGED>(un, nu, bp, ok, qv + 4);
+            if (FORM == kFormGeneral) {
+                rem_group_mixed<N, STAGED>(src + nc, nr, segi * lane_bits, g, k, kl, gbits, rv);
+            } else if (FORM == kFormWindows) {
+                const uint32_t mask = (1u << k) - 1u;
+                uint32_t xw = rx[g];
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    rv[i] = xw & mask;
+                    xw >>= k;
+                }
+            }
+#pragma unroll
+            for (int bb = 0; bb < 8 / N; bb++) {
+                int32_t qq[N];
+                float p[N];
+                uint32_t zb[N];
 #pragma unroll
                 for (int i = 0; i < N; i++)
-                    m[i] = unzigzag(imad(qv[bb * N + i], (N > 1 && i == N - 1) ? pkl : pk, rv[bb * N + i]));
-                L::reinsert(m, 0u, qq);
-            }
-            decoded_point<LAT>(qq, p);
-            if (DITHER) {
-                float d[N];
-                dither_block<LAT>(seed, e0 + (unsigned long long)(32 * q + 8 * g + bb * N), d);
+                    zb[i] = FORM == kFormUnary ? qv[bb * N + i]
+                                               : imad(qv[bb * N + i], (N > 1 && i == N - 1) ? pkl : pk, rv[bb * N + i]);
+                if constexpr (LAT == HQ_E8) {
+                    e8_codes_from_symbols(zb, (coset >> g) & 1u, qq);
+                } else {
+                    int32_t m[N];
 #pragma unroll
-                for (int i = 0; i < N; i++) p[i] = __fsub_rn(p[i], d[i]);
-            }
+                    for (int i = 0; i < N; i++) m[i] = unzigzag(zb[i]);
+                    L::reinsert(m, 0u, qq);
+                }
+                decoded_point<LAT>(qq, p);
+                if (DITHER && LAT != HQ_E8) {
+                    float d[N];
+                    dither_block<LAT>(seed, e0 + (unsigned long long)(32 * q + 8 * g + bb * N), d);
 #pragma unroll
-            for (int i = 0; i < N; i++) u[bb * N + i] = p[i];
+                    for (int i = 0; i < N; i++) p[i] = __fsub_rn(p[i], d[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < N; i++) u[bb * N + i] = p[i];
+            }
         }
+        if constexpr (DITHER && LAT == HQ_E8) {
+            float d[8];
+            e8_dither(z0 + (uint64_t)(4 * g) * kSplitGolden, d);
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float2 x = f2_mul(make_float2(u[2 * j], u[2 * j + 1]), s2);
-            w[4 * g + j] = h2_pack(x.x, x.y);
+            for (int j = 0; j < 4; j++) {
+                const float2 x = f2_fma(make_float2(d[2 * j], d[2 * j + 1]), sd2, f2_mul(make_float2(u[2 * j], u[2 * j + 1]), s2));
+                w[4 * g + j] = h2_pack(x.x, x.y);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float2 x = f2_mul(make_float2(u[2 * j], u[2 * j + 1]), s2);
+                w[4 * g + j] = h2_pack(x.x, x.y);
+            }
         }
     }
     return ok && bp <= nu * 32u;
@@ -249,6 +411,7 @@ struct AttnSmem {
     uint32_t stage[kAttnWarps][2][kAttnStage + kStagePad];
     uint32_t start[kAttnWarps][128];
     uint32_t sign[4];
+    uint32_t pairs[1 << kPairBits];             // E8 at k = 0 (pair_entry)
     float wmax[2][kAttnWarps][R];               // row maxima of each warp's tokens, by parity of the step
     float rescale[R];                           // of the sums, this step
     float qscale[R];                            // undoes a row's power-of-two scale, with the softmax scale
@@ -305,7 +468,7 @@ __device__ __forceinline__ void rotate_query(const AttnArgs &a, float (&u)[4], c
     fwht_row(u, lane);
 }
 
-template <int LAT, bool DITHER, bool GENERAL, int MB>
+template <int LAT, bool DITHER, int FORM, int MB>
 __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     AttnSmem<MB> &sm = *reinterpret_cast<AttnSmem<MB> *>(smem_raw);
@@ -330,6 +493,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
         sm.range[2] = all;
     }
     build_sign_table(sm.sign, 1, a.seed[0]);
+    if (LAT == HQ_E8 && FORM == kFormUnary)
+        for (int i = threadIdx.x; i < (1 << kPairBits); i += blockDim.x) sm.pairs[i] = pair_entry((uint32_t)i);
     for (int r = threadIdx.x; r < R; r += blockDim.x) {
         int64_t pos = INT64_MIN / 2;      // a row past the last sees nothing
         if (row0 + r < a.rows) {
@@ -506,11 +671,11 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
                     const uint32_t segi = 32u * (uint32_t)(cur.r0 + rr) + lane;
                     const unsigned long long e0 = (unsigned long long)(((cur.t0 + ti) * a.heads + head) * kTile);
                     if (staged)
-                        lane_ok = decode_quarter<LAT, DITHER, GENERAL, true>(sm.stage[warp][which], nc, nr, nu, k, kl,
-                                                                             startbit[segi], segi, t4, e0, seed, zs, w);
+                        lane_ok = decode_quarter<LAT, DITHER, FORM, true>(sm.stage[warp][which], nc, nr, nu, k, kl,
+                                                                             startbit[segi], segi, t4, e0, seed, zs, sm.pairs, w);
                     else
-                        lane_ok = decode_quarter<LAT, DITHER, GENERAL, false>(c.src, nc, nr, nu, k, kl, startbit[segi],
-                                                                              segi, t4, e0, seed, zs, w);
+                        lane_ok = decode_quarter<LAT, DITHER, FORM, false>(c.src, nc, nr, nu, k, kl, startbit[segi],
+                                                                              segi, t4, e0, seed, zs, sm.pairs, w);
                 }
                 const unsigned bad_lanes = __ballot_sync(0xffffffffu, valid && !lane_ok);
                 // a tile that did not decode counts as zeros, as a read stores it
@@ -674,9 +839,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
     }
 }
 
-template <int LAT, bool DITHER, bool GENERAL, int MB>
+template <int LAT, bool DITHER, int FORM, int MB>
 cudaError_t launch_mb(const AttnArgs &a, cudaStream_t s) {
-    auto kern = attention_kernel<LAT, DITHER, GENERAL, MB>;
+    auto kern = attention_kernel<LAT, DITHER, FORM, MB>;
     static LaunchPlan plan;
     const size_t smem = sizeof(AttnSmem<MB>);
     unsigned grid = 0;
@@ -689,11 +854,13 @@ cudaError_t launch_mb(const AttnArgs &a, cudaStream_t s) {
 
 template <int LAT, bool DITHER>
 cudaError_t launch_lat(const AttnArgs &a, cudaStream_t s) {
-    // remainders read four windows at a time (k <= 4, one parameter), or bit by bit
+    const bool unary = a.k[0] == 0 && a.k[1] == 0 && a.k_last[0] == 0 && a.k_last[1] == 0;
     const bool general = a.k[0] > 4 || a.k[1] > 4 || a.k_last[0] != a.k[0] || a.k_last[1] != a.k[1];
     const bool small = attn_row_block(a.rows) == 16;
-    if (general) return small ? launch_mb<LAT, DITHER, true, 1>(a, s) : launch_mb<LAT, DITHER, true, 2>(a, s);
-    return small ? launch_mb<LAT, DITHER, false, 1>(a, s) : launch_mb<LAT, DITHER, false, 2>(a, s);
+    if (unary) return small ? launch_mb<LAT, DITHER, kFormUnary, 1>(a, s) : launch_mb<LAT, DITHER, kFormUnary, 2>(a, s);
+    if (general)
+        return small ? launch_mb<LAT, DITHER, kFormGeneral, 1>(a, s) : launch_mb<LAT, DITHER, kFormGeneral, 2>(a, s);
+    return small ? launch_mb<LAT, DITHER, kFormWindows, 1>(a, s) : launch_mb<LAT, DITHER, kFormWindows, 2>(a, s);
 }
 
 }  // namespace

@@ -334,3 +334,20 @@ def test_lse_merges_two_halves():
     assert float((got - o).norm()) <= 3 * (2.0 ** -11 + 2.0 ** -15) * float(T.attend(
         q, T.vectors(a), T.vectors(b), T.seen(1, 128, 0, 0), 2, SCALE)[2].norm())
     assert float((m - l).abs().max()) < 1e-4
+
+
+@pytest.mark.parametrize("k", [0, 1])
+def test_dither_of_many_blocks(k):
+    """A window of one token returns that token's value: half a million E8 blocks, of which some hundred lie so near
+    a border that the fast dither leaves them to the exact one.  A wrong lattice point would move a vector by an
+    eighth of its length and more; fp16 codes by 2^-11."""
+    hq = _hq()
+    heads, n = 4096, 8
+    a, b = T.pair(heads, [n], "E8", k, spare=0)
+    at = hq.KVAttention(a, b, 1, window=1)
+    v = T.vectors(b)
+    q = _queries(1, heads)
+    for t in range(n):
+        out = at(q, torch.empty(1, heads, 128, device="cuda"), length=t + 1)
+        err = (out[0].double() - v[:, t]).norm(dim=-1)
+        assert bool((err <= 2.0 ** -10 * v[:, t].norm(dim=-1)).all())
