@@ -229,6 +229,7 @@ int attend(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *sp, c
             if (w < per_head) per_head = w;
         }
         a.splits = attn_splits(a.heads, a.rows, per_head);
+        a.short_steps = attn_short(a.heads, a.rows, per_head);
         a.part = (float *)workspace;
         a.ml = (float2 *)(a.part + (size_t)a.splits * a.heads * a.row_pad * kTile);
         if (launch_attention(k->params.lattice, k->params.dither, a, s) != cudaSuccess) return HQ_ECUDA;

@@ -35,7 +35,6 @@ namespace hq {
 constexpr int kAttnMaxQueries = 64;   // query tokens of a call (a draft's mask is one word)
 constexpr int kAttnMaxGroup = 64;
 constexpr int kAttnWarps = 8;
-constexpr int kAttnTokens = 16 * kAttnWarps;   // tokens of one step of a CTA: two decoder rounds per warp
 constexpr int kAttnStage = 704;                // staged words of a chunk (5.5 bits per scalar)
 constexpr int kAttnCtas = 2 * 148;             // resident CTAs the splits aim at
 
@@ -52,6 +51,7 @@ struct AttnArgs {
     int64_t len, window, sinks;
     int heads, group, n_q, rows;    // rows = n_q * group query rows per KV head
     int splits, row_pad;            // row_pad: rows rounded up to whole blocks
+    int short_steps;                // a step is one chunk (RW = 1), not four
     float scale_log2;               // scale * log2(e)
     const uint16_t *q;
     int64_t q_ld_tok, q_ld_head;
@@ -75,12 +75,17 @@ cudaError_t launch_attention_e8(int dither, const AttnArgs &a, cudaStream_t s);
 
 // Query rows of one CTA for a call of `rows` rows: blocks of 16 up to 16 rows, of 32 beyond.
 inline int attn_row_block(int rows) { return rows <= 16 ? 16 : 32; }
+// Whether steps are of one chunk, whose rounds four warps share, instead of a chunk to a warp: while
+// that still leaves at most one step to a CTA (short caches, where the time is that of one step).
+inline bool attn_short(int heads, int rows, uint64_t chunks_per_head) {
+    return rows <= 16 && (uint64_t)heads * chunks_per_head <= (uint64_t)kAttnCtas;
+}
 // Splits of the tokens: the CTAs of all heads and row blocks together fill the GPU once.
 inline int attn_splits(int heads, int rows, uint64_t chunks_per_head) {
     const int rb = attn_row_block(rows);
     const int64_t base = (int64_t)heads * ((rows + rb - 1) / rb);
     int64_t s = kAttnCtas / base;
-    const int64_t steps = (int64_t)((2 * chunks_per_head + kAttnWarps - 1) / kAttnWarps);
+    const int64_t steps = (int64_t)(attn_short(heads, rows, chunks_per_head) ? chunks_per_head : (chunks_per_head + 3) / 4);
     if (s > steps) s = steps;
     return (int)(s < 1 ? 1 : s);
 }
@@ -159,35 +164,36 @@ __device__ __forceinline__ uint64_t chunks_before(const AttnArgs &a, int64_t t, 
     return r.base + (in >= r.row.tokens ? r.count : n < r.count ? n : r.count);
 }
 
-// One warp's part of a step: two decoder rounds (16 tokens) of one chunk.
+// One warp's part of a step: a chunk of K or V.
 struct Piece {
-    bool on;              // there is one
-    int r0;               // its first round
-    int n;                // tokens of the chunk
-    int64_t t0;           // position of the chunk's first token
-    float e[2];           // K's and V's scale
-    bool same;            // V's append is K's
-    uint64_t chunk;       // chunk index (K's and V's)
+    bool on, ok;          // there is one; the tables agree on it
+    int n;                // its tokens
+    int64_t t0;           // position of the first
+    float e;              // the append's scale
+    uint64_t w0, w1;      // its words, as the offsets have them
 };
 
 // ------------------------------------------------------------------ E8 dither
-// d = w - Q(w) of dither_block<HQ_E8>, bit for bit, for an eighth of its work.  With w uniform on
-// [0, 4)^8, let c_i = (w_i mod 2) - 1 and b_i = |c_i|: c_i is w_i's residual to the nearest odd
-// integer (candidate B), and c_i - sign(c_i), of size 1 - b_i, the one to the nearest even integer
-// (candidate A).  The squared distances' difference is then linear in the b_i:
-//   (|w - A|^2 - |w - B|^2) / 2 = 4 - sum b + 2 p_A min b - 2 p_B (1 - max b),
-// the last terms being the parity fixes (the largest residual r becomes 2 - r), with the parities
-// of the rounded halves from the two top bits of each w: p_B the XOR of the "w >= 2", p_A of the
-// "1 <= w < 3".  So one pass over c serves both candidates.  Everything is exact in units of 2^-22
-// but the sum (within 16 units).  The reading compares fp32 distances, which are off by less than
-// 2^-16 here (the bound at Lattice<HQ_E8>): a difference within 2^-12, a coordinate on a rounding
-// border (b = 0 or 1) or two equal largest residuals under a fix goes to the reading's own code
-// instead, about one block in 4000.
+// d = w - Q(w) of dither_block<HQ_E8>, bit for bit, in one pass over both candidates.  With w uniform
+// on [0, 4)^8, let c_i be w_i's residual to the nearest even integer (candidate A) and a_i = |c_i|;
+// the one to the nearest odd integer (candidate B) is c_i - sign(c_i), of size 1 - a_i.  The squared
+// distances' difference is then linear in the a_i:
+//   D = (|w - A|^2 - |w - B|^2) / 2 = sum a - 4 + 2 p_A (1 - max a) - 2 p_B min a,
+// the last terms being the parity fixes (the largest residual r becomes 2 - r), with the parities of
+// the rounded halves from the two top bits of each w: p_B the XOR of the "w >= 2", p_A of the
+// "1 <= w < 3".  Everything is exact in units of 2^-22 but the sum (within 16 units).  The reading
+// compares fp32 distances, which are off by less than 2^-16 here (the bound at Lattice<HQ_E8>): a
+// difference within 2^-12, a coordinate on a rounding border (a = 0 or 1) or two equal largest
+// residuals under a fix goes to the reading's own code instead, about one block in 4000.
+//
+// Bound by the ALU pipe (half the FMA pipe's rate), so the conversions run on the XU pipe and the
+// search for the largest residual on the FMA pipe: with sizes in whole units,
+// saturate(size + 1 - largest) is 1 at the largest and 0 elsewhere.
 constexpr float kDitherUnit = 4194304.0f;       // 2^22: d is returned in units of 2^-22
 constexpr uint64_t kSplitGolden = 0x9E3779B97F4A7C15ull;
 
-// Two hashes' worth of a pair: generator state z (s + (i + 1) golden) -> w of the even and the odd
-// coordinate as 32-bit fixed point (bits 8..31 of each count).
+// A pair's hash from its generator state z (s + (i + 1) golden): w of the even and the odd coordinate
+// as 32-bit fixed point (bits 8..31 of each count).
 __device__ __forceinline__ void dither_pair(uint64_t z, uint32_t &even, uint32_t &odd) {
     z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
     z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
@@ -196,31 +202,42 @@ __device__ __forceinline__ void dither_pair(uint64_t z, uint32_t &even, uint32_t
     odd = (uint32_t)z ^ (even << 1);
 }
 
-__device__ __noinline__ void e8_dither_reading(const uint32_t *x, float *d) {
+__device__ __noinline__ void e8_dither_reading(uint64_t z0, float *d) {
     float w[8], p[8];
     int32_t q[8];
-    for (int i = 0; i < 8; i++) w[i] = __fmul_rn((float)(x[i] >> 8), 0x1p-22f);
+    for (int i = 0; i < 4; i++) {
+        uint32_t x, y;
+        dither_pair(z0 + (uint64_t)i * kSplitGolden, x, y);
+        w[2 * i] = __fmul_rn((float)(x >> 8), 0x1p-22f);
+        w[2 * i + 1] = __fmul_rn((float)(y >> 8), 0x1p-22f);
+    }
     Lattice<HQ_E8>::nearest(w, q);
     Lattice<HQ_E8>::point(q, p);
     for (int i = 0; i < 8; i++) d[i] = __fmul_rn(__fsub_rn(w[i], p[i]), kDitherUnit);
 }
 
+__device__ __forceinline__ float add_sat(float a, float b) {
+    float r;
+    asm("add.rn.sat.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // The block whose first pair has generator state z0; d in units of 2^-22.
 __device__ __forceinline__ void e8_dither(uint64_t z0, float (&d)[8]) {
-    uint32_t x[8];
     float c[8];
-#pragma unroll
-    for (int i = 0; i < 4; i++) dither_pair(z0 + (uint64_t)i * kSplitGolden, x[2 * i], x[2 * i + 1]);
+    uint32_t xe = 0, xo = 0;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        // 2^23 + (w mod 2), less 2^23 + 1 (units of 2^-22): exact
-        const float2 f = make_float2(__uint_as_float(((x[2 * i] >> 8) & 0x7FFFFFu) | 0x4B000000u),
-                                     __uint_as_float(((x[2 * i + 1] >> 8) & 0x7FFFFFu) | 0x4B000000u));
-        const float2 r = f2_sub(f, make_float2(8388608.0f + kDitherUnit, 8388608.0f + kDitherUnit));
-        c[2 * i] = r.x;
-        c[2 * i + 1] = r.y;
+        uint32_t x, y;
+        dither_pair(z0 + (uint64_t)i * kSplitGolden, x, y);
+        xe ^= x;
+        xo ^= y;
+        // w mod 2 as a signed fraction: bits 8..30, the border 1 being the lower end
+        c[2 * i] = (float)(int32_t)((x & 0x7FFFFF00u) * 2u);
+        c[2 * i + 1] = (float)(int32_t)((y & 0x7FFFFF00u) * 2u);
     }
-    const uint32_t par = (x[0] ^ x[1] ^ x[2]) ^ (x[3] ^ x[4] ^ x[5]) ^ (x[6] ^ x[7]);
+    constexpr float U = 2147483648.0f;          // here a unit of w is 2^31; sizes are multiples of 2^9
+    const uint32_t par = xe ^ xo;
     const bool pb = (int32_t)par < 0, pa = (int32_t)(par ^ (par << 1)) < 0;
     float lo = fabsf(c[0]), hi = lo;
 #pragma unroll
@@ -230,33 +247,33 @@ __device__ __forceinline__ void e8_dither(uint64_t z0, float (&d)[8]) {
     }
     const float s0 = __fadd_rn(__fadd_rn(fabsf(c[0]), fabsf(c[1])), __fadd_rn(fabsf(c[2]), fabsf(c[3])));
     const float s1 = __fadd_rn(__fadd_rn(fabsf(c[4]), fabsf(c[5])), __fadd_rn(fabsf(c[6]), fabsf(c[7])));
-    const float half = __fsub_rn(__fsub_rn(4.0f * kDitherUnit, s0), s1);
-    const float diff = __fadd_rn(half, __fsub_rn(pa ? __fadd_rn(lo, lo) : 0.0f,
-                                                 pb ? __fmul_rn(2.0f, __fsub_rn(kDitherUnit, hi)) : 0.0f));
+    const float diff = __fadd_rn(__fadd_rn(__fsub_rn(s0, 4.0f * U), s1),
+                                 __fsub_rn(pa ? __fmaf_rn(-2.0f, hi, 2.0f * U) : 0.0f, pb ? __fadd_rn(lo, lo) : 0.0f));
     const bool odd = diff > 0.0f, fix = odd ? pb : pa;
-    // d = c - sign(c) m: m = 0 (B) or 1 (A), and for the coordinate of the fix 2 (B) or -1 (A)
-    const float m0 = odd ? 0.0f : kDitherUnit, m1 = odd ? 2.0f * kDitherUnit : -kDitherUnit;
-    const float at = fix ? (odd ? hi : lo) : -1.0f;
-    float m[8];
+    // sizes with B's sign turned: |c| - m0; the fix takes the largest by 2 the other way
+    const float m0 = odd ? -U : 0.0f, turn = odd ? 2.0f * kDitherUnit : -2.0f * kDitherUnit;
+    const float top = odd ? __fsub_rn(U, lo) : hi;
+    const float shift = fix ? __fsub_rn(1.0f, __fmul_rn(top, 0x1p-9f)) : -INFINITY;
+    float e[8], t[8];
     float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < 8; i++) m[i] = fabsf(c[i]) == at ? m1 : m0;
+    for (int i = 0; i < 8; i++) {
+        t[i] = __fmul_rn(__fadd_rn(fabsf(c[i]), m0), 0x1p-9f);
+        e[i] = add_sat(fabsf(t[i]), shift);
+    }
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        sum = f2_add(sum, make_float2(m[2 * i], m[2 * i + 1]));
-        const float2 r = f2_sub(make_float2(c[2 * i], c[2 * i + 1]),
-                                make_float2(__uint_as_float(__float_as_uint(m[2 * i]) ^ (__float_as_uint(c[2 * i]) & 0x80000000u)),
-                                            __uint_as_float(__float_as_uint(m[2 * i + 1]) ^
-                                                            (__float_as_uint(c[2 * i + 1]) & 0x80000000u))));
-        d[2 * i] = r.x;
-        d[2 * i + 1] = r.y;
+        const float2 e2 = make_float2(e[2 * i], e[2 * i + 1]);
+        sum = f2_add(sum, e2);
+        const float2 r = f2_fma(e2, make_float2(turn, turn), make_float2(t[2 * i], t[2 * i + 1]));
+        d[2 * i] = __uint_as_float(__float_as_uint(r.x) ^ (__float_as_uint(c[2 * i]) & 0x80000000u));
+        d[2 * i + 1] = __uint_as_float(__float_as_uint(r.y) ^ (__float_as_uint(c[2 * i + 1]) & 0x80000000u));
     }
-    const float want = fix ? __fadd_rn(__fmul_rn(7.0f, m0), m1) : __fmul_rn(8.0f, m0);
-    if (fabsf(diff) <= 1024.0f || lo == 0.0f || hi == kDitherUnit || __fadd_rn(sum.x, sum.y) != want) {
-        float t[8];
-        e8_dither_reading(x, t);
+    if (fabsf(diff) <= 0x1p-12f * U || lo == 0.0f || hi == U || __fadd_rn(sum.x, sum.y) != (fix ? 1.0f : 0.0f)) {
+        float r[8];
+        e8_dither_reading(z0, r);
 #pragma unroll
-        for (int i = 0; i < 8; i++) d[i] = t[i];
+        for (int i = 0; i < 8; i++) d[i] = r[i];
     }
 }
 
@@ -401,24 +418,59 @@ __device__ __forceinline__ bool decode_quarter(const uint32_t *src, uint32_t nc,
     return ok && bp <= nu * 32u;
 }
 
+// ------------------------------------------------------------------ segment starts
+// Where each 32-symbol segment of a chunk starts: seg[s] = 32 i + n says that terminator 32 s - 1 is
+// the n-th (0-based) set bit of unary word i.  32 words at a time, a lane to a word: population
+// counts, a scan of two sets packed in one register, and every word that holds a boundary (at most
+// one) notes it; each lane finds the bit itself for the segments it decodes (segment_start).  False
+// unless the plane holds exactly nsym terminators.
+__device__ __forceinline__ bool scan_segments(const uint32_t *un, uint32_t nu, uint32_t nsym, uint32_t *seg, int lane) {
+    uint32_t seen = 0;
+    for (uint32_t i0 = 0; i0 < nu; i0 += 64) {
+        const uint32_t i = i0 + lane;
+        const uint32_t p0 = i < nu ? __popc(un[i]) : 0u, p1 = i + 32u < nu ? __popc(un[i + 32u]) : 0u;
+        uint32_t both = p0 | p1 << 16;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, both, o);
+            if (lane >= o) both += v;
+        }
+        const uint32_t all = __shfl_sync(0xffffffffu, both, 31);
+        const uint32_t b0 = seen + (both & 0xFFFFu) - p0, b1 = seen + (all & 0xFFFFu) + (both >> 16) - p1;
+        // a boundary past the last segment means a corrupt plane: not noted, and found by the count
+        if ((b0 >> 5) != ((b0 + p0) >> 5) && b0 < nsym) seg[(b0 >> 5) + 1u] = i * 32u + (31u - (b0 & 31u));
+        if ((b1 >> 5) != ((b1 + p1) >> 5) && b1 < nsym) seg[(b1 >> 5) + 1u] = (i + 32u) * 32u + (31u - (b1 & 31u));
+        seen += (all & 0xFFFFu) + (all >> 16);
+    }
+    __syncwarp();
+    return seen == nsym;
+}
+__device__ __forceinline__ uint32_t segment_start(const uint32_t *un, const uint32_t *seg, uint32_t s) {
+    if (s == 0u) return 0u;
+    const uint32_t v = seg[s];
+    return (v & ~31u) + select_bit(un[v >> 5], v & 31u) + 1u;
+}
+
 // ------------------------------------------------------------------ shared memory
-template <int MB>
+// MB: blocks of 16 query rows; RW: decoder rounds (8 tokens) of a warp in a step.  Half of the CTA's
+// warps decode K, half V: RW chunks of 32 tokens each in a step.
+template <int MB, int RW>
 struct AttnSmem {
-    static constexpr int R = 16 * MB;
+    static constexpr int R = 16 * MB, NT = 32 * RW, SP = NT + 8;
     uint4 qh[MB * 8 * 32], ql[MB * 8 * 32];     // query fragments (two fp16 parts)
-    uint32_t v[kAttnTokens * 64];               // V: [token][128] fp16, 16-byte pieces swizzled by the token
-    uint32_t p[R * (kAttnTokens / 2)];          // weights: [row][token] fp16, swizzled by the row
+    uint32_t v[NT * 64];                        // V: [token][128] fp16, 16-byte pieces swizzled by the token
+    uint32_t p[R * (NT / 2)];                   // weights: [row][token] fp16, pieces swizzled by the row
+    float sc[R * SP];                           // scores (log2)
     uint32_t stage[kAttnWarps][2][kAttnStage + kStagePad];
-    uint32_t start[kAttnWarps][128];
+    uint32_t seg[kAttnWarps][129];
     uint32_t sign[4];
     uint32_t pairs[1 << kPairBits];             // E8 at k = 0 (pair_entry)
-    float wmax[2][kAttnWarps][R];               // row maxima of each warp's tokens, by parity of the step
     float rescale[R];                           // of the sums, this step
     float qscale[R];                            // undoes a row's power-of-two scale, with the softmax scale
     int64_t qpos[R];
-    float lsum[kAttnWarps][R];
     float xs[kAttnWarps][128];
     uint64_t range[3];
+    int64_t span[2];                            // first and last position of the CTA's queries
     float eref[kAttnWarps];
 };
 
@@ -468,11 +520,12 @@ __device__ __forceinline__ void rotate_query(const AttnArgs &a, float (&u)[4], c
     fwht_row(u, lane);
 }
 
-template <int LAT, bool DITHER, int FORM, int MB>
+template <int LAT, bool DITHER, int FORM, int MB, int RW>
 __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    AttnSmem<MB> &sm = *reinterpret_cast<AttnSmem<MB> *>(smem_raw);
-    constexpr int R = 16 * MB;
+    using Smem = AttnSmem<MB, RW>;
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+    constexpr int R = Smem::R, NT = Smem::NT, SP = Smem::SP, KW = kAttnWarps / 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g8 = lane >> 2, t4 = lane & 3;
     const int split = blockIdx.x, head = blockIdx.y, row0 = blockIdx.z * R;
@@ -491,6 +544,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
         sm.range[0] = ia;
         sm.range[1] = ib;
         sm.range[2] = all;
+        // positions of the block's queries: in order without a tree, at most their count apart with one
+        const int i0 = row0 / a.group, i1 = min(a.rows - 1, row0 + R - 1) / a.group;
+        sm.span[0] = a.mask ? a.len - 1 : a.len - a.n_q + i0;
+        sm.span[1] = a.mask ? a.len - 1 + a.n_q : a.len - a.n_q + i1;
     }
     build_sign_table(sm.sign, 1, a.seed[0]);
     if (LAT == HQ_E8 && FORM == kFormUnary)
@@ -543,7 +600,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
     }
     const uint64_t ia = sm.range[0], ib = sm.range[1], ie = sm.range[2];
     const uint64_t nvis = ia + (ie - ib);
-    const uint64_t steps = (2 * nvis + kAttnWarps - 1) / kAttnWarps;
+    const uint64_t steps = (nvis + RW - 1) / RW;
     // this CTA's steps: an even share
     const uint64_t st0 = steps * (uint64_t)split / (uint64_t)a.splits;
     const uint64_t st1 = steps * (uint64_t)(split + 1) / (uint64_t)a.splits;
@@ -551,7 +608,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
     // ---- V is summed in units of the largest scale among this CTA's appends
     float eref = 0.0f;
     if (st0 < st1) {
-        const uint64_t v0 = st0 * kAttnWarps / 2, v1 = min(nvis, (st1 * kAttnWarps + 1) / 2);
+        const uint64_t v0 = st0 * RW, v1 = min(nvis, st1 * RW);
         AttnRow lo, hi;
         load_row(a, 0, lo);
         hi = lo;
@@ -567,24 +624,31 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
 #pragma unroll
     for (int i = 0; i < kAttnWarps; i++) eref = fmaxf(eref, sm.eref[i]);
 
-    float m_run[MB][2], l_run[MB][2], acc[2 * MB][4];
+    // softmax state of row tid / 16 (+ 16 mb), the same in its 16 threads but for the sums
+    float m_run[MB], l_run[MB], acc[2 * MB][4];
 #pragma unroll
     for (int mb = 0; mb < MB; mb++) {
-        m_run[mb][0] = m_run[mb][1] = kNegInf;
-        l_run[mb][0] = l_run[mb][1] = 0.0f;
+        m_run[mb] = kNegInf;
+        l_run[mb] = 0.0f;
     }
 #pragma unroll
     for (int n = 0; n < 2 * MB; n++) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
 
+    // ---- this warp's part of a step: a chunk (RW = 4) or a round of one (RW = 1), of K or of V
+    const int which = warp / KW, wi = warp % KW;
+    const uint32_t *const words = a.words[which];
+    const uint64_t *const offsets = a.offsets[which];
+    const uint64_t cap = a.cap[which];
+    const int k = a.k[which], kl = a.k_last[which];
+    const uint64_t seed = a.seed[which];
     AttnRow row;
     load_row(a, 0, row);
     auto piece_of = [&](uint64_t step) {
         Piece p;
-        const uint64_t pi = step * kAttnWarps + warp, v = pi >> 1;
+        const uint64_t v = RW == 4 ? step * 4 + wi : step;
         p.on = step < st1 && v < nvis;
-        p.r0 = (int)(pi & 1) * 2;
         p.n = 0;
-        p.same = true;
+        p.w0 = p.w1 = 0;
         if (p.on) {
             const uint64_t i = v < ia ? v : v - ia + ib;
             find_row(a, i, row);
@@ -592,180 +656,175 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
             p.t0 = row.row.token0 + 32 * (int64_t)j;
             const int64_t left = (int64_t)row.row.tokens - 32 * (int64_t)j;
             p.n = (int)(left < 32 ? left : 32);
-            p.on = p.n > 8 * p.r0;
-            p.chunk = row.row.first_chunk + (uint64_t)head * row.count + j;
-            const hq_kv_append_row vr = a.table[1][row.append];
-            p.same = vr.first_chunk == row.row.first_chunk && vr.token0 == row.row.token0 && vr.tokens == row.row.tokens;
-            p.e[0] = row.row.scale_inv;
-            p.e[1] = vr.scale_inv;
+            const uint64_t chunk = row.row.first_chunk + (uint64_t)head * row.count + j;
+            p.e = row.row.scale_inv;
+            p.ok = chunk < a.n_chunks;
+            if (which) {
+                // V's append has to cover the same tokens
+                const hq_kv_append_row vr = a.table[1][row.append];
+                p.ok = p.ok && vr.first_chunk == row.row.first_chunk && vr.token0 == row.row.token0 &&
+                       vr.tokens == row.row.tokens;
+                p.e = vr.scale_inv;
+            }
+            if (p.ok) {
+                p.w0 = offsets[chunk];
+                p.w1 = offsets[chunk + 1];
+            }
         }
         return p;
     };
-    // valid words of a piece's chunk in cache `which`, staged
-    auto words_of = [&](const Piece &p, int which) {
-        ChunkWords cw = {0, 0, false, nullptr, 0, 0};
-        if (p.on && p.chunk < a.n_chunks) {
-            cw.w0 = a.offsets[which][p.chunk];
-            const uint64_t w1 = a.offsets[which][p.chunk + 1];
-            cw.ok = cw.w0 <= w1 && w1 <= a.cap[which] && (which == 0 || p.same);
-            cw.nw = cw.ok ? w1 - cw.w0 : 0ull;
-            cw.src = a.words[which] + cw.w0;
-        }
-        return cw;
-    };
-    auto stage = [&](const ChunkWords &cw, int which) {
-        uint32_t *st = sm.stage[warp][which];
-        if (cw.nw <= (unsigned long long)kAttnStage) {
-            const uint32_t n = (uint32_t)cw.nw;
+    // its words into stage `buf` (nothing for a chunk that is not sound or does not fit)
+    auto stage = [&](const Piece &p, int buf) {
+        uint32_t *st = sm.stage[warp][buf];
+        if (p.on && p.ok && p.w0 <= p.w1 && p.w1 <= cap && p.w1 - p.w0 <= (unsigned long long)kAttnStage) {
+            const uint32_t n = (uint32_t)(p.w1 - p.w0);
+            const uint32_t *src = words + p.w0;
             for (uint32_t i = lane; i < n; i += 32) {
                 const unsigned sa = (unsigned)__cvta_generic_to_shared(st + i);
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(sa), "l"(cw.src + i) : "memory");
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(sa), "l"(src + i) : "memory");
             }
             if (lane < kStagePad) st[n + lane] = 0u;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    uint32_t status[2] = {0u, 0u};
+    uint32_t status = 0u;
+    int buf = 0;
     Piece cur = piece_of(st0);
-    ChunkWords cw[2] = {words_of(cur, 0), words_of(cur, 1)};
-    stage(cw[0], 0);
-    stage(cw[1], 1);
-    for (uint64_t step = st0; step < st1; step++) {
-        const Piece next = piece_of(step + 1);
-        float s[MB][2][4];
-#pragma unroll
-        for (int mb = 0; mb < MB; mb++)
-#pragma unroll
-            for (int rr = 0; rr < 2; rr++) s[mb][rr][0] = s[mb][rr][1] = s[mb][rr][2] = s[mb][rr][3] = 0.0f;
+    stage(cur, 0);
+    Piece next = piece_of(st0 + 1);
+    for (uint64_t step = st0; step < st1; step++, buf ^= 1) {
+        // the next chunk's words behind this one's decode, and the offsets of the one after it
+        stage(next, buf ^ 1);
+        const Piece after = piece_of(step + 2);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        const uint32_t nt = (uint32_t)cur.n, nsym = nt * kTile;
+        const uint32_t nc = (LAT == HQ_E8) ? (16u * nt + 31u) / 32u : 0u;
+        const uint32_t nr = FORM == kFormUnary ? 0u : (nt * tile_rem_bits<Lattice<LAT>::N>(k, kl) + 31u) >> 5;
+        bool ok = cur.on && cur.ok && cur.w0 <= cur.w1 && cur.w1 <= cap;
+        const unsigned long long nw = ok ? cur.w1 - cur.w0 : 0ull;
+        ok = ok && nw >= (unsigned long long)(nc + nr) && (nw - nc - nr) < (unsigned long long)(kMaxUnaryBits / 32u);
+        const uint32_t nu = ok ? (uint32_t)(nw - nc - nr) : 0u;
+        const bool staged = nw <= (unsigned long long)kAttnStage;
+        const uint32_t *const st = sm.stage[warp][buf], *const src = words + cur.w0;
+        uint32_t *const seg = sm.seg[warp];
+        if (staged)
+            ok = scan_segments(st + nc + nr, nu, nsym, seg, lane) && ok;
+        else
+            ok = scan_segments(src + nc + nr, nu, nsym, seg, lane) && ok;
+        const int r0 = RW == 4 ? 0 : wi;
+        // V in units of eref; both in units of 64
+        const float zs = which && cur.on ? __fmul_rn(__fdiv_rn(cur.e, eref), 0.015625f) : 0.015625f;
+        const float ek = cur.on ? __fmul_rn(cur.e, 64.0f) : 0.0f;
+        // every query sees every token of the chunk
+        const int64_t tl = cur.t0 + 31;
+        const bool open = cur.on && cur.n == 32 && tl < a.len && tl <= sm.span[0] &&
+                          (a.window <= 0 || cur.t0 > sm.span[1] - a.window || tl < a.sinks);
+        bool bad = cur.on && !ok;
 #pragma unroll 1
-        for (int which = 0; which < 2; which++) {
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            __syncwarp();
-            const ChunkWords c = which ? cw[1] : cw[0];
-            const int k = which ? a.k[1] : a.k[0], kl = which ? a.k_last[1] : a.k_last[0];
-            const uint64_t seed = which ? a.seed[1] : a.seed[0];
-            const uint32_t nt = (uint32_t)cur.n, nsym = nt * kTile, nseg = 4u * nt;
-            const uint32_t nc = (LAT == HQ_E8) ? (16u * nt + 31u) / 32u : 0u;
-            const uint32_t nr = (nt * tile_rem_bits<Lattice<LAT>::N>(k, kl) + 31u) >> 5;
-            bool ok = cur.on && c.ok && c.nw >= (unsigned long long)(nc + nr) &&
-                      (c.nw - nc - nr) < (unsigned long long)(kMaxUnaryBits / 32u);
-            const uint32_t nu = ok ? (uint32_t)(c.nw - nc - nr) : 0u;
-            const bool staged = c.nw <= (unsigned long long)kAttnStage;
-            uint32_t *startbit = sm.start[warp];
-            if (which == 1) __syncthreads();   // V's and the weights' buffers are free (the last step's sums are done)
-            if (staged)
-                ok = find_segment_starts(sm.stage[warp][which] + nc + nr, nu, nsym, nseg, ok, startbit, lane);
-            else
-                ok = find_segment_starts(c.src + nc + nr, nu, nsym, nseg, ok, startbit, lane);
-            // V in units of eref; both in units of 64
-            const float zs = which && cur.on ? __fmul_rn(__fdiv_rn(cur.e[1], eref), 0.015625f) : 0.015625f;
-            bool bad = cur.on && !ok;
-#pragma unroll 1
-            for (int rr = 0; rr < 2; rr++) {
-                const int ti = 8 * (cur.r0 + rr) + g8;
-                const bool valid = cur.on && ti < cur.n;
-                uint32_t w[16];
-                bool lane_ok = ok;
-                if (ok && valid) {
-                    const uint32_t segi = 32u * (uint32_t)(cur.r0 + rr) + lane;
-                    const unsigned long long e0 = (unsigned long long)(((cur.t0 + ti) * a.heads + head) * kTile);
-                    if (staged)
-                        lane_ok = decode_quarter<LAT, DITHER, FORM, true>(sm.stage[warp][which], nc, nr, nu, k, kl,
-                                                                             startbit[segi], segi, t4, e0, seed, zs, sm.pairs, w);
-                    else
-                        lane_ok = decode_quarter<LAT, DITHER, FORM, false>(c.src, nc, nr, nu, k, kl, startbit[segi],
-                                                                              segi, t4, e0, seed, zs, sm.pairs, w);
-                }
-                const unsigned bad_lanes = __ballot_sync(0xffffffffu, valid && !lane_ok);
-                // a tile that did not decode counts as zeros, as a read stores it
-                const bool zero = !valid || ((bad_lanes >> (lane & ~3)) & 0xFu);
-                bad |= bad_lanes != 0u;
-                if (zero) {
-#pragma unroll
-                    for (int j = 0; j < 16; j++) w[j] = 0u;
-                }
-                if (which == 0) {
-#pragma unroll
-                    for (int st = 0; st < 8; st++) {
-#pragma unroll
-                        for (int mb = 0; mb < MB; mb++) {
-                            const uint4 fh = sm.qh[(mb * 8 + st) * 32 + lane], fl = sm.ql[(mb * 8 + st) * 32 + lane];
-                            const uint32_t ah[4] = {fh.x, fh.y, fh.z, fh.w}, al[4] = {fl.x, fl.y, fl.z, fl.w};
-                            if (rr == 0) {
-                                mma16816(s[mb][0], ah, w[2 * st], w[2 * st + 1]);
-                                mma16816(s[mb][0], al, w[2 * st], w[2 * st + 1]);
-                            } else {
-                                mma16816(s[mb][1], ah, w[2 * st], w[2 * st + 1]);
-                                mma16816(s[mb][1], al, w[2 * st], w[2 * st + 1]);
-                            }
-                        }
-                    }
-                } else {
-                    const int tok = 16 * warp + 8 * rr + g8;
-                    uint4 *dst = reinterpret_cast<uint4 *>(sm.v + tok * 64);
-#pragma unroll
-                    for (int c4 = 0; c4 < 4; c4++)
-                        dst[(4 * t4 + c4) ^ (tok & 7)] = make_uint4(w[4 * c4], w[4 * c4 + 1], w[4 * c4 + 2], w[4 * c4 + 3]);
-                }
+        for (int rr = 0; rr < RW; rr++) {
+            const int ti = 8 * (r0 + rr) + g8;
+            const bool valid = cur.on && ti < cur.n;
+            uint32_t w[16];
+            bool lane_ok = ok;
+            if (ok && valid) {
+                const uint32_t segi = 32u * (uint32_t)(r0 + rr) + lane;
+                const unsigned long long e0 = (unsigned long long)(((cur.t0 + ti) * a.heads + head) * kTile);
+                if (staged)
+                    lane_ok = decode_quarter<LAT, DITHER, FORM, true>(st, nc, nr, nu, k, kl,
+                                                                      segment_start(st + nc + nr, seg, segi), segi, t4, e0,
+                                                                      seed, zs, sm.pairs, w);
+                else
+                    lane_ok = decode_quarter<LAT, DITHER, FORM, false>(src, nc, nr, nu, k, kl,
+                                                                       segment_start(src + nc + nr, seg, segi), segi, t4, e0,
+                                                                       seed, zs, sm.pairs, w);
             }
-            if (bad) status[which] |= HQ_ST_CORRUPT;
-            __syncwarp();
-            // the next piece's words, behind the other cache's decode
-            cw[which] = words_of(next, which);
-            stage(cw[which], which);
+            const unsigned bad_lanes = __ballot_sync(0xffffffffu, valid && !lane_ok);
+            // a tile that did not decode counts as zeros, as a read stores it
+            const bool zero = !valid || ((bad_lanes >> (lane & ~3)) & 0xFu);
+            bad |= bad_lanes != 0u;
+            if (zero) {
+#pragma unroll
+                for (int j = 0; j < 16; j++) w[j] = 0u;
+            }
+            const int tok = (RW == 4 ? 32 * wi + 8 * rr : 8 * wi);   // the round's first token in the step
             if (which == 0) {
-                // scores, masks, and the maximum of each row over this warp's tokens
-                const float ek = cur.on ? __fmul_rn(cur.e[0], 64.0f) : 0.0f;
 #pragma unroll
                 for (int mb = 0; mb < MB; mb++) {
+                    float s[2][4] = {};
+#pragma unroll
+                    for (int st8 = 0; st8 < 8; st8++) {
+                        const uint4 fh = sm.qh[(mb * 8 + st8) * 32 + lane], fl = sm.ql[(mb * 8 + st8) * 32 + lane];
+                        const uint32_t ah[4] = {fh.x, fh.y, fh.z, fh.w}, al[4] = {fl.x, fl.y, fl.z, fl.w};
+                        mma16816(s[0], ah, w[2 * st8], w[2 * st8 + 1]);
+                        mma16816(s[1], al, w[2 * st8], w[2 * st8 + 1]);
+                    }
 #pragma unroll
                     for (int hf = 0; hf < 2; hf++) {
                         const int r = 16 * mb + 8 * hf + g8;
                         const float qs = __fmul_rn(sm.qscale[r], ek);
-                        const int64_t pos = sm.qpos[r];
-                        float top = kNegInf;
+                        float x[2];
 #pragma unroll
-                        for (int rr = 0; rr < 2; rr++) {
-#pragma unroll
-                            for (int cc = 0; cc < 2; cc++) {
-                                const int ti = 8 * (cur.r0 + rr) + 2 * t4 + cc;
-                                const int64_t t = cur.t0 + ti;
-                                const bool see = cur.on && ti < cur.n && t < a.len && t <= pos &&
+                        for (int cc = 0; cc < 2; cc++) {
+                            x[cc] = __fmul_rn(__fadd_rn(s[0][2 * hf + cc], s[1][2 * hf + cc]), qs);
+                            if (!open) {
+                                const int tc = 8 * (r0 + rr) + 2 * t4 + cc;
+                                const int64_t t = cur.t0 + tc, pos = sm.qpos[r];
+                                const bool see = cur.on && tc < cur.n && t < a.len && t <= pos &&
                                                  (a.window <= 0 || t > pos - a.window || t < a.sinks);
-                                float &x = s[mb][rr][2 * hf + cc];
-                                x = see ? __fmul_rn(x, qs) : kNegInf;
-                                top = fmaxf(top, x);
+                                if (!see) x[cc] = kNegInf;
                             }
                         }
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                        if (t4 == 0) sm.wmax[step & 1][warp][r] = top;
+                        *reinterpret_cast<float2 *>(sm.sc + r * SP + tok + 2 * t4) = make_float2(x[0], x[1]);
                     }
                 }
+            } else {
+                uint4 *dst = reinterpret_cast<uint4 *>(sm.v + (tok + g8) * 64);
+#pragma unroll
+                for (int c4 = 0; c4 < 4; c4++)
+                    dst[(4 * t4 + c4) ^ g8] = make_uint4(w[4 * c4], w[4 * c4 + 1], w[4 * c4 + 2], w[4 * c4 + 3]);
             }
         }
-        __syncthreads();   // the row maxima and V are there
+        if (bad) status |= HQ_ST_CORRUPT;
+        __syncthreads();   // scores and V are there
+        {
+            // softmax: 16 threads to a row, NT / 16 tokens each
+            constexpr int PT = NT / 16;
 #pragma unroll
-        for (int mb = 0; mb < MB; mb++) {
+            for (int mb = 0; mb < MB; mb++) {
+                const int r = 16 * mb + (threadIdx.x >> 4), j = threadIdx.x & 15;
+                float x[PT];
+                const float *sc = sm.sc + r * SP + PT * j;
+                if constexpr (PT == 8) {
+                    const float4 y0 = reinterpret_cast<const float4 *>(sc)[0], y1 = reinterpret_cast<const float4 *>(sc)[1];
+                    x[0] = y0.x; x[1] = y0.y; x[2] = y0.z; x[3] = y0.w;
+                    x[4] = y1.x; x[5] = y1.y; x[6] = y1.z; x[7] = y1.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2 *>(sc);
+                    x[0] = y.x; x[1] = y.y;
+                }
+                float m = m_run[mb];
 #pragma unroll
-            for (int hf = 0; hf < 2; hf++) {
-                const int r = 16 * mb + 8 * hf + g8;
-                float m = m_run[mb][hf];
+                for (int i = 0; i < PT; i++) m = fmaxf(m, x[i]);
 #pragma unroll
-                for (int i = 0; i < kAttnWarps; i++) m = fmaxf(m, sm.wmax[step & 1][i][r]);
+                for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                 const float base = m == kNegInf ? 0.0f : m;   // a row that has seen nothing yet: weights exp2(-inf) = 0
-                const float f = ex2(__fsub_rn(m_run[mb][hf], base));
-                m_run[mb][hf] = m;
-                if (warp == 0 && t4 == 0) sm.rescale[r] = f;
+                const float f = ex2(__fsub_rn(m_run[mb], base));
+                m_run[mb] = m;
+                if (j == 0) sm.rescale[r] = f;
                 float sum = 0.0f;
 #pragma unroll
-                for (int rr = 0; rr < 2; rr++) {
-                    const float p0 = ex2(__fsub_rn(s[mb][rr][2 * hf], base)), p1 = ex2(__fsub_rn(s[mb][rr][2 * hf + 1], base));
-                    sum = __fadd_rn(sum, __fadd_rn(p0, p1));
-                    sm.p[r * (kAttnTokens / 2) + 4 * ((2 * warp + rr) ^ (r & 7)) + t4] = h2_pack(p0, p1);
+                for (int i = 0; i < PT; i++) {
+                    x[i] = ex2(__fsub_rn(x[i], base));
+                    sum = __fadd_rn(sum, x[i]);
                 }
-                l_run[mb][hf] = __fmaf_rn(l_run[mb][hf], f, sum);
+                l_run[mb] = __fmaf_rn(l_run[mb], f, sum);
+                if constexpr (PT == 8)
+                    *reinterpret_cast<uint4 *>(sm.p + r * (NT / 2) + 4 * (j ^ (r & 7))) =
+                        make_uint4(h2_pack(x[0], x[1]), h2_pack(x[2], x[3]), h2_pack(x[4], x[5]), h2_pack(x[6], x[7]));
+                else   // four pieces to a row of 32 tokens
+                    sm.p[r * (NT / 2) + 4 * ((j >> 2) ^ ((r >> 1) & 3)) + (j & 3)] = h2_pack(x[0], x[1]);
             }
         }
         __syncthreads();   // the weights are there
@@ -780,21 +839,23 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
                 acc[n][3] = __fmul_rn(acc[n][3], f1);
             }
 #pragma unroll
-            for (int ks = 0; ks < kAttnTokens / 16; ks++) {
+            for (int ks = 0; ks < NT / 16; ks++) {
                 uint32_t av[4];
                 const int tok = 16 * ks + 8 * (lane >> 4) + (lane & 7);
                 ldsm4t(av, sm.v + tok * 64 + 4 * ((2 * warp + ((lane >> 3) & 1)) ^ (tok & 7)));
 #pragma unroll
                 for (int n2 = 0; n2 < MB; n2++) {
                     uint32_t bp[4];
-                    const int r = 16 * n2 + 8 * (lane >> 4) + (lane & 7);
-                    ldsm4(bp, sm.p + r * (kAttnTokens / 2) + 4 * ((2 * ks + ((lane >> 3) & 1)) ^ (r & 7)));
+                    const int r = 16 * n2 + 8 * (lane >> 4) + (lane & 7), piece = 2 * ks + ((lane >> 3) & 1);
+                    ldsm4(bp, sm.p + r * (NT / 2) + 4 * (RW == 4 ? piece ^ (r & 7) : piece ^ ((r >> 1) & 3)));
                     mma16816(acc[2 * n2], av, bp[0], bp[1]);
                     mma16816(acc[2 * n2 + 1], av, bp[2], bp[3]);
                 }
             }
         }
+        __syncthreads();   // V, the scores and the weights may be written again
         cur = next;
+        next = after;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 
@@ -811,39 +872,20 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
     }
 #pragma unroll
     for (int mb = 0; mb < MB; mb++) {
+        float l = l_run[mb];
 #pragma unroll
-        for (int hf = 0; hf < 2; hf++) {
-            float l = l_run[mb][hf];
-            l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 1));
-            l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 2));
-            if (t4 == 0) sm.lsum[warp][16 * mb + 8 * hf + g8] = l;
-        }
+        for (int o = 1; o < 16; o <<= 1) l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, o));
+        if ((threadIdx.x & 15) == 0) a.ml[pbase + 16 * mb + (threadIdx.x >> 4)] = make_float2(m_run[mb], l);
     }
-    __syncthreads();
-    if (warp == 0 && t4 == 0) {
-#pragma unroll
-        for (int mb = 0; mb < MB; mb++) {
-#pragma unroll
-            for (int hf = 0; hf < 2; hf++) {
-                const int r = 16 * mb + 8 * hf + g8;
-                float l = 0.0f;
-                for (int i = 0; i < kAttnWarps; i++) l = __fadd_rn(l, sm.lsum[i][r]);
-                a.ml[pbase + r] = make_float2(m_run[mb][hf], l);
-            }
-        }
-    }
-#pragma unroll
-    for (int which = 0; which < 2; which++) {
-        const uint32_t st = __reduce_or_sync(0xffffffffu, status[which]);
-        if (lane == 0 && st) atomicOr(&a.stats[which]->status, st);
-    }
+    status = __reduce_or_sync(0xffffffffu, status);
+    if (lane == 0 && status) atomicOr(&a.stats[which]->status, status);
 }
 
-template <int LAT, bool DITHER, int FORM, int MB>
-cudaError_t launch_mb(const AttnArgs &a, cudaStream_t s) {
-    auto kern = attention_kernel<LAT, DITHER, FORM, MB>;
+template <int LAT, bool DITHER, int FORM, int MB, int RW>
+cudaError_t launch_rw(const AttnArgs &a, cudaStream_t s) {
+    auto kern = attention_kernel<LAT, DITHER, FORM, MB, RW>;
     static LaunchPlan plan;
-    const size_t smem = sizeof(AttnSmem<MB>);
+    const size_t smem = sizeof(AttnSmem<MB, RW>);
     unsigned grid = 0;
     cudaError_t e = plan.grid(kern, kAttnWarps * 32, smem, 1, grid);
     if (e != cudaSuccess) return e;
@@ -852,15 +894,18 @@ cudaError_t launch_mb(const AttnArgs &a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <int LAT, bool DITHER, int FORM>
+cudaError_t launch_form(const AttnArgs &a, cudaStream_t s) {
+    if (attn_row_block(a.rows) == 32) return launch_rw<LAT, DITHER, FORM, 2, 4>(a, s);
+    return a.short_steps ? launch_rw<LAT, DITHER, FORM, 1, 1>(a, s) : launch_rw<LAT, DITHER, FORM, 1, 4>(a, s);
+}
+
 template <int LAT, bool DITHER>
 cudaError_t launch_lat(const AttnArgs &a, cudaStream_t s) {
-    const bool unary = a.k[0] == 0 && a.k[1] == 0 && a.k_last[0] == 0 && a.k_last[1] == 0;
-    const bool general = a.k[0] > 4 || a.k[1] > 4 || a.k_last[0] != a.k[0] || a.k_last[1] != a.k[1];
-    const bool small = attn_row_block(a.rows) == 16;
-    if (unary) return small ? launch_mb<LAT, DITHER, kFormUnary, 1>(a, s) : launch_mb<LAT, DITHER, kFormUnary, 2>(a, s);
-    if (general)
-        return small ? launch_mb<LAT, DITHER, kFormGeneral, 1>(a, s) : launch_mb<LAT, DITHER, kFormGeneral, 2>(a, s);
-    return small ? launch_mb<LAT, DITHER, kFormWindows, 1>(a, s) : launch_mb<LAT, DITHER, kFormWindows, 2>(a, s);
+    if (a.k[0] == 0 && a.k[1] == 0 && a.k_last[0] == 0 && a.k_last[1] == 0) return launch_form<LAT, DITHER, kFormUnary>(a, s);
+    if (a.k[0] > 4 || a.k[1] > 4 || a.k_last[0] != a.k[0] || a.k_last[1] != a.k[1])
+        return launch_form<LAT, DITHER, kFormGeneral>(a, s);
+    return launch_form<LAT, DITHER, kFormWindows>(a, s);
 }
 
 }  // namespace
