@@ -144,11 +144,6 @@ int check_spec(const hq_attn_spec *sp) {
     return HQ_OK;
 }
 
-int row_pad_of(int rows) {
-    const int rb = attn_row_block(rows);
-    return (rows + rb - 1) / rb * rb;
-}
-
 int attend(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *sp, const void *d_q, int64_t q_ld_token,
            int64_t q_ld_head, bool tree, const void *d_kd, const void *d_vd, int64_t d_ld_token, int64_t d_ld_head,
            const uint64_t *d_mask, void *out, int out_dtype, int64_t out_ld_token, int64_t out_ld_head, float *d_lse,
@@ -200,7 +195,7 @@ int attend(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *sp, c
     a.group = sp->group;
     a.n_q = sp->n_q;
     a.rows = sp->n_q * sp->group;
-    a.row_pad = row_pad_of(a.rows);
+    a.row_pad = attn_row_pad(a.rows);
     a.scale = sp->scale;
     a.scale_log2 = (float)((double)sp->scale * 1.4426950408889634074);
     a.q = (const uint16_t *)d_q;
@@ -264,7 +259,7 @@ int hq_kv_attention_workspace_bytes(int32_t heads, const hq_attn_spec *spec, siz
     const int rows = spec->n_q * spec->group;
     // as many splits as any cache of this many heads may take
     const size_t splits = (size_t)attn_splits(heads, rows, UINT64_C(1) << 40);
-    *bytes = (splits * (size_t)heads * (size_t)row_pad_of(rows) * (kTile * sizeof(float) + sizeof(float2)) + 255) &
+    *bytes = (splits * (size_t)heads * (size_t)attn_row_pad(rows) * (kTile * sizeof(float) + sizeof(float2)) + 255) &
              ~(size_t)255;
     return HQ_OK;
 }

@@ -50,7 +50,7 @@ struct AttnArgs {
     uint64_t n_chunks, n_appends;
     int64_t len, window, sinks;
     int heads, group, n_q, rows;    // rows = n_q * group query rows per KV head
-    int splits, row_pad;            // row_pad: rows rounded up to whole blocks
+    int splits, row_pad;            // row_pad: rows of a head in `part`
     int short_steps;                // a step is one chunk (RW = 1), not four
     float scale_log2;               // scale * log2(e)
     const uint16_t *q;
@@ -73,18 +73,18 @@ cudaError_t launch_attention_a2(int dither, const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_attention_d4(int dither, const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_attention_e8(int dither, const AttnArgs &a, cudaStream_t s);
 
-// Query rows of one CTA for a call of `rows` rows: blocks of 16 up to 16 rows, of 32 beyond.
-inline int attn_row_block(int rows) { return rows <= 16 ? 16 : 32; }
+// Query rows of one CTA: one block of 16 (attention_kernel), or up to 256 in blocks of 128 (attention_wide).
+constexpr int kNarrowRows = 16;
+inline int attn_row_pad(int rows) { return rows <= kNarrowRows ? 16 : (rows + 127) / 128 * 128; }
 // Whether steps are of one chunk, whose rounds four warps share, instead of a chunk to a warp: while
 // that still leaves at most one step to a CTA (short caches, where the time is that of one step).
 inline bool attn_short(int heads, int rows, uint64_t chunks_per_head) {
-    return rows <= 16 && (uint64_t)heads * chunks_per_head <= (uint64_t)kAttnCtas;
+    return rows <= kNarrowRows && (uint64_t)heads * chunks_per_head <= (uint64_t)kAttnCtas;
 }
 // Splits of the tokens: the CTAs of all heads and row blocks together fill the GPU once.
 inline int attn_splits(int heads, int rows, uint64_t chunks_per_head) {
-    const int rb = attn_row_block(rows);
-    const int64_t base = (int64_t)heads * ((rows + rb - 1) / rb);
-    int64_t s = kAttnCtas / base;
+    const int64_t base = rows <= kNarrowRows ? heads : (int64_t)heads * ((rows + 255) / 256);
+    int64_t s = (rows <= kNarrowRows ? kAttnCtas : kAttnCtas / 2) / base;
     const int64_t steps = (int64_t)(attn_short(heads, rows, chunks_per_head) ? chunks_per_head : (chunks_per_head + 3) / 4);
     if (s > steps) s = steps;
     return (int)(s < 1 ? 1 : s);
@@ -520,134 +520,104 @@ __device__ __forceinline__ void rotate_query(const AttnArgs &a, float (&u)[4], c
     fwht_row(u, lane);
 }
 
-template <int LAT, bool DITHER, int FORM, int MB, int RW>
-__global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __grid_constant__ AttnArgs a) {
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    using Smem = AttnSmem<MB, RW>;
-    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
-    constexpr int R = Smem::R, NT = Smem::NT, SP = Smem::SP, KW = kAttnWarps / 2;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g8 = lane >> 2, t4 = lane & 3;
-    const int split = blockIdx.x, head = blockIdx.y, row0 = blockIdx.z * R;
+// ------------------------------------------------------------------ what both kernels share
+// Chunks of a head that some query may see: [0, range[0]) and [range[1], range[2]).
+__device__ __forceinline__ void visible_range(const AttnArgs &a, uint64_t *range) {
+    const int64_t pmin = a.mask ? a.len - 1 : a.len - a.n_q;   // of any query: a bound is enough here
+    const uint64_t all = chunks_before(a, a.len, true);
+    uint64_t ia = all, ib = all;
+    if (a.window > 0) {
+        ia = a.sinks > 0 ? chunks_before(a, a.sinks < a.len ? a.sinks : a.len, true) : 0;
+        const int64_t lo = pmin - a.window + 1;
+        ib = lo > 0 ? chunks_before(a, lo, false) : 0;
+        if (ib < ia) ib = ia;
+    }
+    range[0] = ia;
+    range[1] = ib;
+    range[2] = all;
+}
+// Bounds of the positions of query rows [row0, row0 + n): in order without a tree, at most their count
+// apart with one.
+__device__ __forceinline__ void query_span(const AttnArgs &a, int row0, int n, int64_t *span) {
+    const int i0 = row0 / a.group, i1 = min(a.rows - 1, row0 + n - 1) / a.group;
+    span[0] = a.mask ? a.len - 1 : a.len - a.n_q + i0;
+    span[1] = a.mask ? a.len - 1 + a.n_q : a.len - a.n_q + i1;
+}
+// Position of a query row; one past the last sees nothing.
+__device__ __forceinline__ int64_t query_position(const AttnArgs &a, int row) {
+    if (row >= a.rows) return INT64_MIN / 2;
+    const int i = row / a.group;
+    if (!a.mask) return a.len - a.n_q + i;
+    const unsigned long long all = a.n_q < 64 ? (1ull << a.n_q) - 1ull : ~0ull;
+    return a.len - 1 + __popcll(a.mask[i] & all);
+}
+// A query row, rotated, times the power of two that brings its largest value into [1, 2) (rows of zeros,
+// infinities: 1), 4 coordinates to a lane; up: the power's inverse.  Whole warp.
+__device__ __forceinline__ void load_query(const AttnArgs &a, int head, int row, const uint32_t *sign, float *xs, int lane,
+                                           float (&u)[4], float &up) {
+    u[0] = u[1] = u[2] = u[3] = 0.0f;
+    if (row < a.rows) {
+        const int i = row / a.group, qh = head * a.group + row - i * a.group;
+        const uint2 x = *reinterpret_cast<const uint2 *>(a.q + i * a.q_ld_tok + qh * a.q_ld_head + 4 * lane);
+        u[0] = __uint_as_float(x.x << 16);
+        u[1] = __uint_as_float(x.x & 0xFFFF0000u);
+        u[2] = __uint_as_float(x.y << 16);
+        u[3] = __uint_as_float(x.y & 0xFFFF0000u);
+    }
+    rotate_query(a, u, sign, xs, lane);
+    float top = fmaxf(fmaxf(fabsf(u[0]), fabsf(u[1])), fmaxf(fabsf(u[2]), fabsf(u[3])));
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+    const int ex = (int)(__float_as_uint(top) >> 23) - 127;
+    const bool in = ex >= -126 && ex <= 126;
+    const float down = in ? __uint_as_float((uint32_t)(127 - ex) << 23) : 1.0f;
+    up = in ? __uint_as_float((uint32_t)(127 + ex) << 23) : 1.0f;
+#pragma unroll
+    for (int j = 0; j < 4; j++) u[j] = __fmul_rn(u[j], down);
+}
+// The largest of V's scales among the appends of visible chunks [v0, v1), over a warp (each warp takes its
+// share of the appends; the caller joins them): V is summed in its units.
+__device__ __forceinline__ float reference_scale(const AttnArgs &a, uint64_t nvis, uint64_t ia, uint64_t ib, uint64_t v0,
+                                                 uint64_t v1) {
+    float e = 0.0f;
+    if (v0 >= v1) return e;
+    AttnRow lo, hi;
+    load_row(a, 0, lo);
+    hi = lo;
+    find_row(a, v0 < ia ? v0 : v0 - ia + ib, lo);
+    find_row(a, v1 - 1 < ia ? v1 - 1 : v1 - 1 - ia + ib, hi);
+    for (uint64_t i = lo.append + threadIdx.x; i <= hi.append; i += blockDim.x) e = fmaxf(e, a.table[1][i].scale_inv);
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, m));
+    return e;
+}
 
-    // ---- which chunks the queries can see, the queries themselves
-    if (threadIdx.x == 0) {
-        const int64_t pmin = a.mask ? a.len - 1 : a.len - a.n_q;   // of any query: a bound is enough here
-        const uint64_t all = chunks_before(a, a.len, true);
-        uint64_t ia = all, ib = all;
-        if (a.window > 0) {
-            ia = a.sinks > 0 ? chunks_before(a, a.sinks < a.len ? a.sinks : a.len, true) : 0;
-            const int64_t lo = pmin - a.window + 1;
-            ib = lo > 0 ? chunks_before(a, lo, false) : 0;
-            if (ib < ia) ib = ia;
-        }
-        sm.range[0] = ia;
-        sm.range[1] = ib;
-        sm.range[2] = all;
-        // positions of the block's queries: in order without a tree, at most their count apart with one
-        const int i0 = row0 / a.group, i1 = min(a.rows - 1, row0 + R - 1) / a.group;
-        sm.span[0] = a.mask ? a.len - 1 : a.len - a.n_q + i0;
-        sm.span[1] = a.mask ? a.len - 1 + a.n_q : a.len - a.n_q + i1;
-    }
-    build_sign_table(sm.sign, 1, a.seed[0]);
-    if (LAT == HQ_E8 && FORM == kFormUnary)
-        for (int i = threadIdx.x; i < (1 << kPairBits); i += blockDim.x) sm.pairs[i] = pair_entry((uint32_t)i);
-    for (int r = threadIdx.x; r < R; r += blockDim.x) {
-        int64_t pos = INT64_MIN / 2;      // a row past the last sees nothing
-        if (row0 + r < a.rows) {
-            const int i = (row0 + r) / a.group;
-            pos = a.len - a.n_q + i;
-            if (a.mask) {
-                const unsigned long long all = a.n_q < 64 ? (1ull << a.n_q) - 1ull : ~0ull;
-                pos = a.len - 1 + __popcll(a.mask[i] & all);
-            }
-        }
-        sm.qpos[r] = pos;
-    }
-    __syncthreads();
-    for (int r = warp; r < R; r += kAttnWarps) {
-        float u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (row0 + r < a.rows) {
-            const int i = (row0 + r) / a.group, qh = head * a.group + (row0 + r) - i * a.group;
-            const uint2 x = *reinterpret_cast<const uint2 *>(a.q + i * a.q_ld_tok + qh * a.q_ld_head + 4 * lane);
-            u[0] = __uint_as_float(x.x << 16);
-            u[1] = __uint_as_float(x.x & 0xFFFF0000u);
-            u[2] = __uint_as_float(x.y << 16);
-            u[3] = __uint_as_float(x.y & 0xFFFF0000u);
-        }
-        rotate_query(a, u, sm.sign, sm.xs[warp], lane);
-        float top = fmaxf(fmaxf(fabsf(u[0]), fabsf(u[1])), fmaxf(fabsf(u[2]), fabsf(u[3])));
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-        // power of two that brings the row's largest value into [1, 2) (rows of zeros, infinities: 1)
-        const int ex = (int)(__float_as_uint(top) >> 23) - 127;
-        const float down = (ex >= -126 && ex <= 126) ? __uint_as_float((uint32_t)(127 - ex) << 23) : 1.0f;
-        const float up = (ex >= -126 && ex <= 126) ? __uint_as_float((uint32_t)(127 + ex) << 23) : 1.0f;
-        // fragment of coordinate c for row r: step s = (c mod 32) / 4 of lane quarter c / 32
-#pragma unroll
-        for (int pr = 0; pr < 2; pr++) {
-            const float x0 = __fmul_rn(u[2 * pr], down), x1 = __fmul_rn(u[2 * pr + 1], down);
-            const uint32_t hi = h2_pack(x0, x1);
-            const __half2 hh = *reinterpret_cast<const __half2 *>(&hi);
-            const uint32_t lo = h2_pack(__fsub_rn(x0, __low2float(hh)), __fsub_rn(x1, __high2float(hh)));
-            // coordinates 4 lane + 2 pr: quarter lane / 8, step lane % 8, register pair pr
-            const int slot = ((r >> 4) * 8 + (lane & 7)) * 32 + (r & 7) * 4 + (lane >> 3);
-            const int reg = ((r >> 3) & 1) + 2 * pr;
-            reinterpret_cast<uint32_t *>(sm.qh)[slot * 4 + reg] = hi;
-            reinterpret_cast<uint32_t *>(sm.ql)[slot * 4 + reg] = lo;
-        }
-        if (lane == 0) sm.qscale[r] = __fmul_rn(up, a.scale_log2);
-    }
-    const uint64_t ia = sm.range[0], ib = sm.range[1], ie = sm.range[2];
-    const uint64_t nvis = ia + (ie - ib);
-    const uint64_t steps = (nvis + RW - 1) / RW;
-    // this CTA's steps: an even share
-    const uint64_t st0 = steps * (uint64_t)split / (uint64_t)a.splits;
-    const uint64_t st1 = steps * (uint64_t)(split + 1) / (uint64_t)a.splits;
-
-    // ---- V is summed in units of the largest scale among this CTA's appends
-    float eref = 0.0f;
-    if (st0 < st1) {
-        const uint64_t v0 = st0 * RW, v1 = min(nvis, st1 * RW);
-        AttnRow lo, hi;
-        load_row(a, 0, lo);
-        hi = lo;
-        find_row(a, v0 < ia ? v0 : v0 - ia + ib, lo);
-        find_row(a, v1 - 1 < ia ? v1 - 1 : v1 - 1 - ia + ib, hi);
-        for (uint64_t i = lo.append + threadIdx.x; i <= hi.append; i += blockDim.x)
-            eref = fmaxf(eref, a.table[1][i].scale_inv);
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) eref = fmaxf(eref, __shfl_xor_sync(0xffffffffu, eref, m));
-    }
-    if (lane == 0) sm.eref[warp] = eref;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kAttnWarps; i++) eref = fmaxf(eref, sm.eref[i]);
-
-    // softmax state of row tid / 16 (+ 16 mb), the same in its 16 threads but for the sums
-    float m_run[MB], l_run[MB], acc[2 * MB][4];
-#pragma unroll
-    for (int mb = 0; mb < MB; mb++) {
-        m_run[mb] = kNegInf;
-        l_run[mb] = 0.0f;
-    }
-#pragma unroll
-    for (int n = 0; n < 2 * MB; n++) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-
-    // ---- this warp's part of a step: a chunk (RW = 4) or a round of one (RW = 1), of K or of V
-    const int which = warp / KW, wi = warp % KW;
-    const uint32_t *const words = a.words[which];
-    const uint64_t *const offsets = a.offsets[which];
-    const uint64_t cap = a.cap[which];
-    const int k = a.k[which], kl = a.k_last[which];
-    const uint64_t seed = a.seed[which];
+// The cache that a warp decodes: K (0) or V (1).
+struct Source {
+    const uint32_t *words;
+    const uint64_t *offsets;
+    uint64_t cap, seed;
+    int which, k, kl;
     AttnRow row;
-    load_row(a, 0, row);
-    auto piece_of = [&](uint64_t step) {
+    __device__ __forceinline__ void init(const AttnArgs &a, int w) {
+        which = w;
+        words = a.words[w];
+        offsets = a.offsets[w];
+        cap = a.cap[w];
+        seed = a.seed[w];
+        k = a.k[w];
+        kl = a.k_last[w];
+        load_row(a, 0, row);
+    }
+    // visible chunk v
+    __device__ __forceinline__ Piece piece(const AttnArgs &a, int head, uint64_t v, bool on, uint64_t nvis, uint64_t ia,
+                                           uint64_t ib) {
         Piece p;
-        const uint64_t v = RW == 4 ? step * 4 + wi : step;
-        p.on = step < st1 && v < nvis;
+        p.on = on && v < nvis;
+        p.ok = false;
         p.n = 0;
+        p.t0 = 0;
+        p.e = 0.0f;
         p.w0 = p.w1 = 0;
         if (p.on) {
             const uint64_t i = v < ia ? v : v - ia + ib;
@@ -672,55 +642,147 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
             }
         }
         return p;
-    };
-    // its words into stage `buf` (nothing for a chunk that is not sound or does not fit)
-    auto stage = [&](const Piece &p, int buf) {
-        uint32_t *st = sm.stage[warp][buf];
+    }
+    // its words into a stage, by `of` threads (nothing for a chunk that is not sound or does not fit)
+    __device__ __forceinline__ void stage(const Piece &p, uint32_t *st, int me, int of) const {
         if (p.on && p.ok && p.w0 <= p.w1 && p.w1 <= cap && p.w1 - p.w0 <= (unsigned long long)kAttnStage) {
             const uint32_t n = (uint32_t)(p.w1 - p.w0);
             const uint32_t *src = words + p.w0;
-            for (uint32_t i = lane; i < n; i += 32) {
+            for (uint32_t i = me; i < n; i += of) {
                 const unsigned sa = (unsigned)__cvta_generic_to_shared(st + i);
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(sa), "l"(src + i) : "memory");
             }
-            if (lane < kStagePad) st[n + lane] = 0u;
+            if (me < kStagePad) st[n + me] = 0u;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-    };
+    }
+};
+// A piece's planes, in words.
+struct Planes {
+    uint32_t nc, nr, nu, nsym;
+    bool ok, staged;
+    template <int LAT, int FORM>
+    __device__ __forceinline__ void init(const Source &s, const Piece &p) {
+        const uint32_t nt = (uint32_t)p.n;
+        nsym = nt * kTile;
+        nc = (LAT == HQ_E8) ? (16u * nt + 31u) / 32u : 0u;
+        nr = FORM == kFormUnary ? 0u : (nt * tile_rem_bits<Lattice<LAT>::N>(s.k, s.kl) + 31u) >> 5;
+        ok = p.on && p.ok && p.w0 <= p.w1 && p.w1 <= s.cap;
+        const unsigned long long nw = ok ? p.w1 - p.w0 : 0ull;
+        ok = ok && nw >= (unsigned long long)(nc + nr) && (nw - nc - nr) < (unsigned long long)(kMaxUnaryBits / 32u);
+        nu = ok ? (uint32_t)(nw - nc - nr) : 0u;
+        staged = nw <= (unsigned long long)kAttnStage;
+    }
+};
+// Whether every query sees every token of a whole chunk.
+__device__ __forceinline__ bool all_see(const AttnArgs &a, const Piece &p, const int64_t *span) {
+    const int64_t tl = p.t0 + 31;
+    return p.on && p.n == 32 && tl < a.len && tl <= span[0] &&
+           (a.window <= 0 || p.t0 > span[1] - a.window || tl < a.sinks);
+}
+// A tile that did not decode (one of its four lanes) or is not there counts as zeros, as a read stores it;
+// whether the warp saw one that did not.
+__device__ __forceinline__ bool zero_bad_tiles(bool valid, bool lane_ok, int lane, uint32_t (&w)[16]) {
+    const unsigned bad_lanes = __ballot_sync(0xffffffffu, valid && !lane_ok);
+    if (!valid || ((bad_lanes >> (lane & ~3)) & 0xFu)) {
+#pragma unroll
+        for (int j = 0; j < 16; j++) w[j] = 0u;
+    }
+    return bad_lanes != 0u;
+}
 
+template <int LAT, bool DITHER, int FORM, int MB, int RW>
+__global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __grid_constant__ AttnArgs a) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    using Smem = AttnSmem<MB, RW>;
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+    constexpr int R = Smem::R, NT = Smem::NT, SP = Smem::SP, KW = kAttnWarps / 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g8 = lane >> 2, t4 = lane & 3;
+    const int split = blockIdx.x, head = blockIdx.y, row0 = blockIdx.z * R;
+
+    // ---- which chunks the queries can see, the queries themselves
+    if (threadIdx.x == 0) {
+        visible_range(a, sm.range);
+        query_span(a, row0, R, sm.span);
+    }
+    build_sign_table(sm.sign, 1, a.seed[0]);
+    if (LAT == HQ_E8 && FORM == kFormUnary)
+        for (int i = threadIdx.x; i < (1 << kPairBits); i += blockDim.x) sm.pairs[i] = pair_entry((uint32_t)i);
+    for (int r = threadIdx.x; r < R; r += blockDim.x) sm.qpos[r] = query_position(a, row0 + r);
+    __syncthreads();
+    for (int r = warp; r < R; r += kAttnWarps) {
+        float u[4], up;
+        load_query(a, head, row0 + r, sm.sign, sm.xs[warp], lane, u, up);
+        // fragment of coordinate c for row r: step s = (c mod 32) / 4 of lane quarter c / 32
+#pragma unroll
+        for (int pr = 0; pr < 2; pr++) {
+            const float x0 = u[2 * pr], x1 = u[2 * pr + 1];
+            const uint32_t hi = h2_pack(x0, x1);
+            const __half2 hh = *reinterpret_cast<const __half2 *>(&hi);
+            const uint32_t lo = h2_pack(__fsub_rn(x0, __low2float(hh)), __fsub_rn(x1, __high2float(hh)));
+            // coordinates 4 lane + 2 pr: quarter lane / 8, step lane % 8, register pair pr
+            const int slot = ((r >> 4) * 8 + (lane & 7)) * 32 + (r & 7) * 4 + (lane >> 3);
+            const int reg = ((r >> 3) & 1) + 2 * pr;
+            reinterpret_cast<uint32_t *>(sm.qh)[slot * 4 + reg] = hi;
+            reinterpret_cast<uint32_t *>(sm.ql)[slot * 4 + reg] = lo;
+        }
+        if (lane == 0) sm.qscale[r] = __fmul_rn(up, a.scale_log2);
+    }
+    const uint64_t ia = sm.range[0], ib = sm.range[1], ie = sm.range[2];
+    const uint64_t nvis = ia + (ie - ib);
+    const uint64_t steps = (nvis + RW - 1) / RW;
+    // this CTA's steps: an even share
+    const uint64_t st0 = steps * (uint64_t)split / (uint64_t)a.splits;
+    const uint64_t st1 = steps * (uint64_t)(split + 1) / (uint64_t)a.splits;
+
+    // ---- V is summed in units of the largest scale among this CTA's appends
+    float eref = reference_scale(a, nvis, ia, ib, st0 * RW, min(nvis, st1 * RW));
+    if (lane == 0) sm.eref[warp] = eref;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAttnWarps; i++) eref = fmaxf(eref, sm.eref[i]);
+
+    // softmax state of row tid / 16 (+ 16 mb), the same in its 16 threads but for the sums
+    float m_run[MB], l_run[MB], acc[2 * MB][4];
+#pragma unroll
+    for (int mb = 0; mb < MB; mb++) {
+        m_run[mb] = kNegInf;
+        l_run[mb] = 0.0f;
+    }
+#pragma unroll
+    for (int n = 0; n < 2 * MB; n++) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+
+    // ---- this warp's part of a step: a chunk (RW = 4) or a round of one (RW = 1), of K or of V
+    const int which = warp / KW, wi = warp % KW, ci = RW == 4 ? wi : 0;
+    Source src;
+    src.init(a, which);
     uint32_t status = 0u;
     int buf = 0;
-    Piece cur = piece_of(st0);
-    stage(cur, 0);
-    Piece next = piece_of(st0 + 1);
+    Piece cur = src.piece(a, head, st0 * RW + ci, st0 < st1, nvis, ia, ib);
+    src.stage(cur, sm.stage[warp][0], lane, 32);
+    Piece next = src.piece(a, head, (st0 + 1) * RW + ci, st0 + 1 < st1, nvis, ia, ib);
     for (uint64_t step = st0; step < st1; step++, buf ^= 1) {
         // the next chunk's words behind this one's decode, and the offsets of the one after it
-        stage(next, buf ^ 1);
-        const Piece after = piece_of(step + 2);
+        src.stage(next, sm.stage[warp][buf ^ 1], lane, 32);
+        const Piece after = src.piece(a, head, (step + 2) * RW + ci, step + 2 < st1, nvis, ia, ib);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
-        const uint32_t nt = (uint32_t)cur.n, nsym = nt * kTile;
-        const uint32_t nc = (LAT == HQ_E8) ? (16u * nt + 31u) / 32u : 0u;
-        const uint32_t nr = FORM == kFormUnary ? 0u : (nt * tile_rem_bits<Lattice<LAT>::N>(k, kl) + 31u) >> 5;
-        bool ok = cur.on && cur.ok && cur.w0 <= cur.w1 && cur.w1 <= cap;
-        const unsigned long long nw = ok ? cur.w1 - cur.w0 : 0ull;
-        ok = ok && nw >= (unsigned long long)(nc + nr) && (nw - nc - nr) < (unsigned long long)(kMaxUnaryBits / 32u);
-        const uint32_t nu = ok ? (uint32_t)(nw - nc - nr) : 0u;
-        const bool staged = nw <= (unsigned long long)kAttnStage;
-        const uint32_t *const st = sm.stage[warp][buf], *const src = words + cur.w0;
+        Planes pl;
+        pl.template init<LAT, FORM>(src, cur);
+        const bool staged = pl.staged;
+        const uint32_t *const st = sm.stage[warp][buf], *const gsrc = src.words + cur.w0;
         uint32_t *const seg = sm.seg[warp];
+        bool ok = pl.ok;
         if (staged)
-            ok = scan_segments(st + nc + nr, nu, nsym, seg, lane) && ok;
+            ok = scan_segments(st + pl.nc + pl.nr, pl.nu, pl.nsym, seg, lane) && ok;
         else
-            ok = scan_segments(src + nc + nr, nu, nsym, seg, lane) && ok;
+            ok = scan_segments(gsrc + pl.nc + pl.nr, pl.nu, pl.nsym, seg, lane) && ok;
         const int r0 = RW == 4 ? 0 : wi;
         // V in units of eref; both in units of 64
         const float zs = which && cur.on ? __fmul_rn(__fdiv_rn(cur.e, eref), 0.015625f) : 0.015625f;
         const float ek = cur.on ? __fmul_rn(cur.e, 64.0f) : 0.0f;
-        // every query sees every token of the chunk
-        const int64_t tl = cur.t0 + 31;
-        const bool open = cur.on && cur.n == 32 && tl < a.len && tl <= sm.span[0] &&
-                          (a.window <= 0 || cur.t0 > sm.span[1] - a.window || tl < a.sinks);
+        const bool open = all_see(a, cur, sm.span);
         bool bad = cur.on && !ok;
 #pragma unroll 1
         for (int rr = 0; rr < RW; rr++) {
@@ -732,22 +794,15 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
                 const uint32_t segi = 32u * (uint32_t)(r0 + rr) + lane;
                 const unsigned long long e0 = (unsigned long long)(((cur.t0 + ti) * a.heads + head) * kTile);
                 if (staged)
-                    lane_ok = decode_quarter<LAT, DITHER, FORM, true>(st, nc, nr, nu, k, kl,
-                                                                      segment_start(st + nc + nr, seg, segi), segi, t4, e0,
-                                                                      seed, zs, sm.pairs, w);
+                    lane_ok = decode_quarter<LAT, DITHER, FORM, true>(st, pl.nc, pl.nr, pl.nu, src.k, src.kl,
+                                                                      segment_start(st + pl.nc + pl.nr, seg, segi), segi,
+                                                                      t4, e0, src.seed, zs, sm.pairs, w);
                 else
-                    lane_ok = decode_quarter<LAT, DITHER, FORM, false>(src, nc, nr, nu, k, kl,
-                                                                       segment_start(src + nc + nr, seg, segi), segi, t4, e0,
-                                                                       seed, zs, sm.pairs, w);
+                    lane_ok = decode_quarter<LAT, DITHER, FORM, false>(gsrc, pl.nc, pl.nr, pl.nu, src.k, src.kl,
+                                                                       segment_start(gsrc + pl.nc + pl.nr, seg, segi), segi,
+                                                                       t4, e0, src.seed, zs, sm.pairs, w);
             }
-            const unsigned bad_lanes = __ballot_sync(0xffffffffu, valid && !lane_ok);
-            // a tile that did not decode counts as zeros, as a read stores it
-            const bool zero = !valid || ((bad_lanes >> (lane & ~3)) & 0xFu);
-            bad |= bad_lanes != 0u;
-            if (zero) {
-#pragma unroll
-                for (int j = 0; j < 16; j++) w[j] = 0u;
-            }
+            bad |= zero_bad_tiles(valid, lane_ok, lane, w);
             const int tok = (RW == 4 ? 32 * wi + 8 * rr : 8 * wi);   // the round's first token in the step
             if (which == 0) {
 #pragma unroll
@@ -881,6 +936,379 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
     if (lane == 0 && status) atomicOr(&a.stats[which]->status, status);
 }
 
+// ------------------------------------------------------------------ many rows
+// attention_wide: up to 256 query rows of a KV head in one CTA (draft trees), so that a token is decoded
+// once for all of them.  16 warps, one CTA per SM; a step is four chunks (128 tokens), decoded by 8 warps
+// for K and 8 for V (two to a chunk, two rounds each) into two shared-memory tiles, [token][128] fp16 in
+// panels of 64 coordinates with the 128-byte swizzle.  The products run on tcgen05 with their sums in
+// TMEM, a block of 128 rows at a time:
+//   S (128 rows x 128 tokens) = Q K^T, Q as two fp16: the upper part from shared memory, the lower
+//     part from TMEM, K with the contracted coordinate contiguous;
+//   O (128 rows x 128 coordinates) += P V, P in fp16 from TMEM over S's columns, V as it lies (the
+//     contracted token in steps of 128 bytes).
+// TMEM: O of both blocks (256 columns), S / P (128), Q's lower part (2 x 64): all 512.
+// Softmax: a thread holds 32 tokens (one chunk) of one row; four threads share a row and exchange their
+// maxima through shared memory.  A row's maximum is moved only when a new one is 2^8 larger, so O is
+// hardly ever rescaled; weights then reach 2^8, still far inside fp16.
+constexpr int kWideThreads = 512;
+constexpr int kWideRows = 256;
+constexpr uint32_t kWaitLimit = 1u << 20;   // polls of 1 us before the kernel gives up (HQ_ST_TIMEOUT)
+constexpr float kLazyMax = 8.0f;
+
+struct WideInfo {
+    int64_t t0;
+    float ek;
+    int n, open;
+};
+struct WideSmem {
+    uint4 qh[2][2048];                          // upper part of Q: [block][panel][row][8 pieces], swizzled
+    uint4 k[2048], v[2048];                     // [panel][token][8 pieces], swizzled
+    uint32_t stage[kAttnWarps][2][kAttnStage + kStagePad];   // per chunk of a step (4 of K, 4 of V)
+    uint32_t seg[16][132];
+    uint32_t pairs[1 << kPairBits];
+    float qscale[kWideRows];
+    int64_t qpos[kWideRows];
+    float mx[4][128];
+    WideInfo info[4];
+    uint64_t bar[2];                            // S is there; O is there
+    uint64_t range[3];
+    int64_t span[2];
+    float eref[16];
+    uint32_t sign[4];
+    uint32_t tmem;
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
+    const uint32_t a = smem_u32(bar);
+    for (uint32_t i = 0; i < kWaitLimit; i++) {
+        uint32_t done;
+        asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
+                     : "=r"(done) : "r"(a), "r"(parity), "r"(1000u) : "memory");
+        if (done) return true;
+    }
+    return false;
+}
+// Shared-memory operand descriptor, 128-byte swizzle: strides in bytes.
+__device__ __forceinline__ uint64_t smem_desc(const void *p, uint32_t lead, uint32_t stride) {
+    return (uint64_t)((smem_u32(p) & 0x3FFFFu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
+           1ull << 46 | 2ull << 61;
+}
+// fp16 x fp16 -> fp32, M = N = 128; the second operand with the contracted index contiguous or not.
+constexpr uint32_t kIdescK = 1u << 4 | (128u >> 3) << 17 | (128u >> 4) << 24;
+constexpr uint32_t kIdescMN = kIdescK | 1u << 16;
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t at) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+                 "%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(at) : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+                 "%29,%30,%31,%32};"
+                 ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                   "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+                   "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+                   "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]) : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                   "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+template <int LAT, bool DITHER, int FORM>
+__global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_constant__ AttnArgs a) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    // the swizzle counts from 1024-byte lines
+    WideSmem &sm = *reinterpret_cast<WideSmem *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g8 = lane >> 2, t4 = lane & 3;
+    const int split = blockIdx.x, head = blockIdx.y, row0 = blockIdx.z * kWideRows;
+    const int rows = min(a.rows - row0, kWideRows), nb = rows > 128 ? 2 : 1;
+
+    if (threadIdx.x == 0) {
+        visible_range(a, sm.range);
+        query_span(a, row0, rows, sm.span);
+        for (int i = 0; i < 2; i++)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&sm.bar[i])) : "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    build_sign_table(sm.sign, 1, a.seed[0]);
+    if (LAT == HQ_E8 && FORM == kFormUnary)
+        for (int i = threadIdx.x; i < (1 << kPairBits); i += blockDim.x) sm.pairs[i] = pair_entry((uint32_t)i);
+    for (int r = threadIdx.x; r < kWideRows; r += blockDim.x) sm.qpos[r] = query_position(a, row0 + r);
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tm = sm.tmem, tmS = tm + 256u, tmQ = tm + 384u;
+    const uint32_t lane_base = (uint32_t)(warp & 3) << 21;   // this warp's 32 TMEM lanes (lane in bits 16..)
+
+    // ---- queries: upper parts to their tiles, lower parts through the K and V tiles to TMEM
+    for (int r = warp; r < 128 * nb; r += 16) {
+        float u[4], up;
+        load_query(a, head, row0 + r, sm.sign, reinterpret_cast<float *>(sm.seg[warp]), lane, u, up);
+        const uint32_t h0 = h2_pack(u[0], u[1]), h1 = h2_pack(u[2], u[3]);
+        const __half2 a0 = *reinterpret_cast<const __half2 *>(&h0), a1 = *reinterpret_cast<const __half2 *>(&h1);
+        const uint32_t l0 = h2_pack(__fsub_rn(u[0], __low2float(a0)), __fsub_rn(u[1], __high2float(a0)));
+        const uint32_t l1 = h2_pack(__fsub_rn(u[2], __low2float(a1)), __fsub_rn(u[3], __high2float(a1)));
+        // coordinates 4 lane ..: panel lane / 16, piece (lane mod 16) / 2 of 8 coordinates, half lane & 1
+        const int b = r >> 7, rr = r & 127;
+        uint2 *qh = reinterpret_cast<uint2 *>(&sm.qh[b][(lane >> 4) * 1024 + rr * 8 + (((lane & 15) >> 1) ^ (rr & 7))]);
+        qh[lane & 1] = make_uint2(h0, h1);
+        uint2 *ql = reinterpret_cast<uint2 *>(&(b ? sm.v : sm.k)[rr * 16 + ((lane >> 1) ^ (rr & 15))]);
+        ql[lane & 1] = make_uint2(l0, l1);
+        if (lane == 0) sm.qscale[r] = __fmul_rn(up, a.scale_log2);
+    }
+    __syncthreads();
+    const int row = (warp & 3) * 32 + lane, grp = warp >> 2;   // this thread's row of a block, and its quarter of the tokens
+    for (int b = 0; b < nb; b++) {
+        uint32_t r[16];
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            const uint4 x = (b ? sm.v : sm.k)[row * 16 + ((4 * grp + c) ^ (row & 15))];
+            r[4 * c] = x.x; r[4 * c + 1] = x.y; r[4 * c + 2] = x.z; r[4 * c + 3] = x.w;
+        }
+        tmem_st16(tmQ + 64u * b + 16u * grp + lane_base, r);
+    }
+    const uint64_t ia = sm.range[0], ib = sm.range[1], ie = sm.range[2];
+    const uint64_t nvis = ia + (ie - ib), steps = (nvis + 3) / 4;
+    const uint64_t st0 = steps * (uint64_t)split / (uint64_t)a.splits;
+    const uint64_t st1 = steps * (uint64_t)(split + 1) / (uint64_t)a.splits;
+    float eref = reference_scale(a, nvis, ia, ib, st0 * 4, min(nvis, st1 * 4));
+    if (lane == 0) sm.eref[warp] = eref;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; i++) eref = fmaxf(eref, sm.eref[i]);
+
+    const int which = warp >> 3, ci = (warp & 7) >> 1, r0 = 2 * (warp & 1), chunk_slot = 4 * which + ci;
+    Source src;
+    src.init(a, which);
+    float m_run[2] = {kNegInf, kNegInf}, l_run[2] = {0.0f, 0.0f};
+    uint32_t status = 0u;
+    bool dead = false;
+    int buf = 0;
+    uint32_t s_count = 0;   // commits of S so far
+    Piece cur = src.piece(a, head, st0 * 4 + ci, st0 < st1, nvis, ia, ib);
+    src.stage(cur, sm.stage[chunk_slot][0], threadIdx.x & 63, 64);
+    Piece next = src.piece(a, head, (st0 + 1) * 4 + ci, st0 + 1 < st1, nvis, ia, ib);
+    for (uint64_t step = st0; step < st1; step++, buf ^= 1) {
+        src.stage(next, sm.stage[chunk_slot][buf ^ 1], threadIdx.x & 63, 64);
+        const Piece after = src.piece(a, head, (step + 2) * 4 + ci, step + 2 < st1, nvis, ia, ib);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        // the chunk's words come from both of its warps
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + chunk_slot) : "memory");
+        Planes pl;
+        pl.template init<LAT, FORM>(src, cur);
+        const bool staged = pl.staged;
+        const uint32_t *const st = sm.stage[chunk_slot][buf], *const gsrc = src.words + cur.w0;
+        uint32_t *const seg = sm.seg[warp];
+        bool ok = pl.ok;
+        if (staged)
+            ok = scan_segments(st + pl.nc + pl.nr, pl.nu, pl.nsym, seg, lane) && ok;
+        else
+            ok = scan_segments(gsrc + pl.nc + pl.nr, pl.nu, pl.nsym, seg, lane) && ok;
+        if (which == 0 && r0 == 0 && lane == 0) {
+            WideInfo &w = sm.info[ci];
+            w.t0 = cur.t0;
+            w.n = cur.on ? cur.n : 0;
+            w.ek = cur.on ? __fmul_rn(cur.e, 64.0f) : 0.0f;
+            w.open = all_see(a, cur, sm.span);
+        }
+        // V's tile is free when the last step's sums are done
+        if (which == 1 && step > st0) dead |= !bar_wait(&sm.bar[1], (uint32_t)(step - st0 - 1) & 1u);
+        const float zs = which && cur.on ? __fmul_rn(__fdiv_rn(cur.e, eref), 0.015625f) : 0.015625f;
+        uint4 *const tile = which ? sm.v : sm.k;
+        bool bad = cur.on && !ok;
+#pragma unroll 1
+        for (int rr = 0; rr < 2; rr++) {
+            const int ti = 8 * (r0 + rr) + g8;
+            const bool valid = cur.on && ti < cur.n;
+            uint32_t w[16];
+            bool lane_ok = ok;
+            if (ok && valid) {
+                const uint32_t segi = 32u * (uint32_t)(r0 + rr) + lane;
+                const unsigned long long e0 = (unsigned long long)(((cur.t0 + ti) * a.heads + head) * kTile);
+                if (staged)
+                    lane_ok = decode_quarter<LAT, DITHER, FORM, true>(st, pl.nc, pl.nr, pl.nu, src.k, src.kl,
+                                                                      segment_start(st + pl.nc + pl.nr, seg, segi), segi,
+                                                                      t4, e0, src.seed, zs, sm.pairs, w);
+                else
+                    lane_ok = decode_quarter<LAT, DITHER, FORM, false>(gsrc, pl.nc, pl.nr, pl.nu, src.k, src.kl,
+                                                                       segment_start(gsrc + pl.nc + pl.nr, seg, segi), segi,
+                                                                       t4, e0, src.seed, zs, sm.pairs, w);
+            }
+            bad |= zero_bad_tiles(valid, lane_ok, lane, w);
+            // token 32 ci + ti: panel t4 / 2, pieces 4 (t4 & 1) ..
+            const int t = 32 * ci + ti;
+#pragma unroll
+            for (int c4 = 0; c4 < 4; c4++)
+                tile[(t4 >> 1) * 1024 + t * 8 + ((4 * (t4 & 1) + c4) ^ (t & 7))] =
+                    make_uint4(w[4 * c4], w[4 * c4 + 1], w[4 * c4 + 2], w[4 * c4 + 3]);
+        }
+        if (bad) status |= HQ_ST_CORRUPT;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        dead = __syncthreads_or(dead);   // K, V and the chunks' records are there
+        if (dead) break;
+        auto issue_s = [&](int b) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ks++) {
+                const int at = (ks >> 2) * 1024 + (ks & 3) * 2;
+                umma_ss(tmS, smem_desc(&sm.qh[b][at], 16, 1024), smem_desc(&sm.k[at], 16, 1024), kIdescK, ks > 0);
+            }
+#pragma unroll
+            for (int ks = 0; ks < 8; ks++)
+                umma_ts(tmS, tmQ + 64u * b + 8u * ks, smem_desc(&sm.k[(ks >> 2) * 1024 + (ks & 3) * 2], 16, 1024), kIdescK, true);
+            umma_commit(&sm.bar[0]);
+        };
+        if (threadIdx.x == 0) {
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            issue_s(0);
+        }
+        const WideInfo info = sm.info[grp];
+        for (int b = 0; b < nb; b++) {
+            dead |= !bar_wait(&sm.bar[0], s_count & 1u);
+            s_count++;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const bool live = 128 * b + (warp & 3) * 32 < rows;   // rows past the last are left out
+            const int r = 128 * b + row;
+            float x[32], top = kNegInf;
+            if (live) {
+                uint32_t raw[32];
+                tmem_ld32(raw, tmS + 32u * grp + lane_base);
+                const float qs = __fmul_rn(sm.qscale[r], info.ek);
+#pragma unroll
+                for (int i = 0; i < 32; i++) x[i] = __fmul_rn(__uint_as_float(raw[i]), qs);
+                if (!info.open) {
+                    const int64_t pos = sm.qpos[r];
+#pragma unroll
+                    for (int i = 0; i < 32; i++) {
+                        const int64_t t = info.t0 + i;
+                        const bool see = i < info.n && t < a.len && t <= pos &&
+                                         (a.window <= 0 || t > pos - a.window || t < a.sinks);
+                        if (!see) x[i] = kNegInf;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 32; i++) top = fmaxf(top, x[i]);
+                sm.mx[grp][row] = top;
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            dead = __syncthreads_or(dead);
+            if (dead) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (live) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) top = fmaxf(top, sm.mx[i][row]);
+                float m = b ? m_run[1] : m_run[0], l = b ? l_run[1] : l_run[0], f = 1.0f;
+                if (top > __fadd_rn(m, kLazyMax) || (m == kNegInf && top != kNegInf)) {
+                    f = m == kNegInf ? 0.0f : ex2(__fsub_rn(m, top));
+                    m = top;
+                }
+                if (__any_sync(0xffffffffu, f != 1.0f) && step > st0) {
+                    // the sums of the last step are there: its barrier has been passed or is passed here
+                    dead |= !bar_wait(&sm.bar[1], (uint32_t)(step - st0 - 1) & 1u);
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    uint32_t o[32];
+                    tmem_ld32(o, tm + 128u * b + 32u * grp + lane_base);
+#pragma unroll
+                    for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__fmul_rn(__uint_as_float(o[i]), f));
+                    tmem_st32(tm + 128u * b + 32u * grp + lane_base, o);
+                }
+                const float base = m == kNegInf ? 0.0f : m;
+                uint32_t pw[16];
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const float p0 = ex2(__fsub_rn(x[2 * i], base)), p1 = ex2(__fsub_rn(x[2 * i + 1], base));
+                    sum = __fadd_rn(sum, __fadd_rn(p0, p1));
+                    pw[i] = h2_pack(p0, p1);
+                }
+                l = __fmaf_rn(l, f, sum);
+                m_run[b ? 1 : 0] = m;
+                l_run[b ? 1 : 0] = l;
+                tmem_st16(tmS + 16u * grp + lane_base, pw);
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            dead = __syncthreads_or(dead);
+            if (dead) break;
+            if (threadIdx.x == 0) {
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+                for (int ks = 0; ks < 8; ks++)
+                    umma_ts(tm + 128u * b, tmS + 8u * ks, smem_desc(&sm.v[ks * 128], 16384, 1024), kIdescMN,
+                            step > st0 || ks > 0);
+                if (b + 1 < nb)
+                    issue_s(b + 1);   // after the product above has read the weights in its place
+                else
+                    umma_commit(&sm.bar[1]);
+            }
+        }
+        if (dead) break;   // the same in all threads: the barriers above
+        cur = next;
+        next = after;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (st0 < st1 && !dead) dead = !bar_wait(&sm.bar[1], (uint32_t)(st1 - st0 - 1) & 1u);
+    dead = __syncthreads_or(dead);
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+
+    // ---- the split's partial results
+    const float eo = __fmul_rn(eref, 64.0f);
+    for (int b = 0; b < nb; b++) {
+        const bool live = 128 * b + (warp & 3) * 32 < rows;
+        const int64_t at = ((int64_t)split * a.heads + head) * a.row_pad + row0 + 128 * b + row;
+        if (live) {
+            uint32_t o[32] = {};
+            if (st0 < st1 && !dead) tmem_ld32(o, tm + 128u * b + 32u * grp + lane_base);
+            float4 *dst = reinterpret_cast<float4 *>(a.part + at * kTile + 32 * grp);
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                dst[i] = make_float4(__fmul_rn(__uint_as_float(o[4 * i]), eo), __fmul_rn(__uint_as_float(o[4 * i + 1]), eo),
+                                     __fmul_rn(__uint_as_float(o[4 * i + 2]), eo), __fmul_rn(__uint_as_float(o[4 * i + 3]), eo));
+            sm.mx[grp][row] = b ? l_run[1] : l_run[0];
+        }
+        __syncthreads();
+        if (live && grp == 0)
+            a.ml[at] = make_float2(b ? m_run[1] : m_run[0],
+                                   __fadd_rn(__fadd_rn(sm.mx[0][row], sm.mx[1][row]), __fadd_rn(sm.mx[2][row], sm.mx[3][row])));
+        __syncthreads();
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (warp == 0) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
+    }
+    if (dead) status |= HQ_ST_TIMEOUT;
+    status = __reduce_or_sync(0xffffffffu, status);
+    if (lane == 0 && status) atomicOr(&a.stats[which]->status, status);
+}
+
 template <int LAT, bool DITHER, int FORM, int MB, int RW>
 cudaError_t launch_rw(const AttnArgs &a, cudaStream_t s) {
     auto kern = attention_kernel<LAT, DITHER, FORM, MB, RW>;
@@ -895,8 +1323,21 @@ cudaError_t launch_rw(const AttnArgs &a, cudaStream_t s) {
 }
 
 template <int LAT, bool DITHER, int FORM>
+cudaError_t launch_wide(const AttnArgs &a, cudaStream_t s) {
+    auto kern = attention_wide<LAT, DITHER, FORM>;
+    static LaunchPlan plan;
+    const size_t smem = sizeof(WideSmem) + 1024;   // room to align
+    unsigned grid = 0;
+    cudaError_t e = plan.grid(kern, kWideThreads, smem, 1, grid);
+    if (e != cudaSuccess) return e;
+    const dim3 g((unsigned)a.splits, (unsigned)a.heads, (unsigned)((a.rows + kWideRows - 1) / kWideRows));
+    kern<<<g, kWideThreads, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int LAT, bool DITHER, int FORM>
 cudaError_t launch_form(const AttnArgs &a, cudaStream_t s) {
-    if (attn_row_block(a.rows) == 32) return launch_rw<LAT, DITHER, FORM, 2, 4>(a, s);
+    if (a.rows > kNarrowRows) return launch_wide<LAT, DITHER, FORM>(a, s);
     return a.short_steps ? launch_rw<LAT, DITHER, FORM, 1, 1>(a, s) : launch_rw<LAT, DITHER, FORM, 1, 4>(a, s);
 }
 
