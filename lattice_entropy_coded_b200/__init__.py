@@ -171,8 +171,8 @@ def _ptr(t) -> int | None:
 
 
 def _stream(s) -> int | None:
-    if s is None:
-        return torch.cuda.current_stream().cuda_stream
+    if s is None:   # the current stream of the current device (torch.cuda.current_stream() takes 3 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(s, torch.cuda.Stream):
         return s.cuda_stream
     return int(s)
@@ -485,24 +485,28 @@ def hq_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, spec: hq_rop
     """q, q_out bf16 [tokens, heads_q, 128]; k, k_out bf16 [heads_k, tokens, 128] (the layout hq_kv_append
     takes); any strides, the last 1.  inv_freq fp64 [rot_dim / 2]; positions int64 [tokens] or None
     (pos0 + t); wq, wk bf16 [128] or None."""
-    tokens = q.shape[0] if q is not None else k.shape[1] if k is not None else 0
-    for t, o, tok in ((q, q_out, 0), (k, k_out, 1)):
-        if t is None:
+    bf16 = torch.bfloat16
+    tokens, side = None, []
+    for x, o, w, t in ((q, q_out, wq, 0), (k, k_out, wk, 1)):   # t: the dimension of the tokens
+        if x is None:
+            side.append((None, 0, 0, 0, None, None, 0, 0))
             continue
-        assert t.dtype == o.dtype == torch.bfloat16 and t.shape == o.shape and t.dim() == 3
-        assert t.shape[2] == 128 and t.stride(2) == 1 and o.stride(2) == 1 and t.shape[tok] == tokens
-    assert spec.rot_dim == 0 or (inv_freq.dtype == torch.float64 and inv_freq.is_contiguous()
-                                 and inv_freq.numel() == spec.rot_dim // 2)
-    for w in (wq, wk):
-        assert w is None or (w.dtype == torch.bfloat16 and w.is_contiguous() and w.numel() == 128)
-    assert positions is None or (positions.dtype == torch.int64 and positions.is_contiguous()
-                                 and positions.numel() == tokens)
-    qs, qo = ((t.stride(0), t.stride(1)) if t is not None else (0, 0) for t in (q, q_out))
-    ks, ko = ((t.stride(1), t.stride(0)) if t is not None else (0, 0) for t in (k, k_out))
-    return _check(_lib.hq_qk_norm_rope(_ptr(q), *qs, q.shape[1] if q is not None else 0, _ptr(k), *ks,
-                                       k.shape[0] if k is not None else 0, tokens, C.byref(spec), _ptr(wq), _ptr(wk),
-                                       _ptr(inv_freq), _ptr(positions), int(pos0), _ptr(q_out), *qo, _ptr(k_out), *ko,
-                                       _stream(cuda_stream)), "hq_qk_norm_rope")
+        shape, xs, os_ = x.shape, x.stride(), o.stride()
+        assert x.dtype is bf16 and o.dtype is bf16 and len(shape) == 3 and shape[2] == 128 and shape == o.shape
+        assert xs[2] == 1 and os_[2] == 1 and (tokens is None or tokens == shape[t])
+        assert w is None or (w.dtype is bf16 and w.numel() == 128 and w.is_contiguous())
+        tokens = shape[t]
+        side.append((x.data_ptr(), xs[t], xs[1 - t], shape[1 - t], None if w is None else w.data_ptr(), o.data_ptr(),
+                     os_[t], os_[1 - t]))
+    tokens = tokens or 0
+    assert spec.rot_dim <= 0 or (inv_freq.dtype is torch.float64 and inv_freq.numel() == spec.rot_dim // 2
+                                 and inv_freq.is_contiguous())
+    assert positions is None or (positions.dtype is torch.int64 and positions.numel() == tokens
+                                 and positions.is_contiguous())
+    (qp, qt, qh, nq, wqp, qo, qot, qoh), (kp, kt, kh, nk, wkp, ko, kot, koh) = side
+    return _check(_lib.hq_qk_norm_rope(qp, qt, qh, nq, kp, kt, kh, nk, tokens, C.byref(spec), wqp, wkp, _ptr(inv_freq),
+                                       _ptr(positions), pos0, qo, qot, qoh, ko, kot, koh, _stream(cuda_stream)),
+                  "hq_qk_norm_rope")
 
 
 # ------------------------------------------------------------------ torch-allocated wrappers

@@ -11,8 +11,8 @@
 // The pass is bound by its bytes (2 read, 2 written per element, 6 operations): half a
 // warp holds a head vector, 8 elements to a lane in two 8-byte pieces that are both ends of
 // 4 pairs, so the rotation needs no exchange and the norm four shuffles.  A half-warp keeps
-// its token's 4 angles and walks over heads, so the sines cost one evaluation per token and
-// lane; short calls spread a token's heads over more half-warps instead.
+// its token's 4 angles and the side's 8 weights and walks over heads, so the sines cost one
+// evaluation per token and lane; short calls spread a token's heads over more half-warps instead.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -51,17 +51,24 @@ __device__ __forceinline__ uint32_t bf_pack(float a, float b) {
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
-// The lane's 8 elements: 4 pairs (a, b), pair u at coordinates pa(u), pb(u), and the index of its
-// angle (pairs past rot_dim / 2 do not turn).  VEC: the a's and the b's are each one aligned run of
-// four, or (interleaved) the pairs one run of eight; otherwise (rot_dim % 8 != 0) single elements.
-template <bool VEC>
-struct PairMap {
-    int oa, ob;   // VEC: first coordinates of the two runs of four
-    int pair0;    // VEC: index of the lane's first pair
+// The lane's 8 elements are 4 pairs (a, b).  kHalves, kPairs (rot_dim % 8 == 0): the a's and the b's
+// are each an aligned run of four, or the pairs one run of eight; the pairs that do not turn are such
+// runs too.  kSingles: any other rot_dim, element by element.
+enum RopeForm { kHalves = 0, kPairs = 1, kSingles = 2 };
+
+template <int FORM>
+__device__ __forceinline__ int pair_of(int j, int u) { return FORM == kSingles ? j + 16 * u : 4 * j + u; }
+
+struct Lane8 {
+    float2 a[2], b[2];   // pairs 0..3: (a0, a1), (a2, a3) and the b's
+};
+template <int FORM>
+struct LaneMap {
+    int oa, ob;       // first coordinates of the two runs of four
+    int ca[4], cb[4]; // kSingles: the coordinates
     __device__ __forceinline__ void init(const RopeArgs &a, int j) {
         const int half = a.rot >> 1;
-        pair0 = 4 * j;
-        if (a.interleaved) {
+        if (FORM == kPairs) {
             oa = 8 * j;
             ob = 8 * j + 4;
         } else if (4 * j < half) {
@@ -71,142 +78,146 @@ struct PairMap {
             oa = a.rot + 8 * (j - half / 4);
             ob = oa + 4;
         }
+        if (FORM == kSingles) {
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                const int p = pair_of<FORM>(j, u);
+                const bool halves = !a.interleaved && p < half;
+                ca[u] = halves ? p : 2 * p;
+                cb[u] = halves ? p + half : 2 * p + 1;
+            }
+        }
     }
-    __device__ __forceinline__ static int pair(int j, int u) { return VEC ? 4 * j + u : j + 16 * u; }
-    __device__ __forceinline__ static int pa(const RopeArgs &a, int p) {
-        const int half = a.rot >> 1;
-        return a.interleaved ? 2 * p : p < half ? p : 2 * p;
+    __device__ __forceinline__ Lane8 load(const uint16_t *x) const {
+        Lane8 r;
+        if (FORM == kSingles) {
+            float f[8];
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                f[u] = __uint_as_float((uint32_t)x[ca[u]] << 16);
+                f[4 + u] = __uint_as_float((uint32_t)x[cb[u]] << 16);
+            }
+            r.a[0] = make_float2(f[0], f[1]);
+            r.a[1] = make_float2(f[2], f[3]);
+            r.b[0] = make_float2(f[4], f[5]);
+            r.b[1] = make_float2(f[6], f[7]);
+            return r;
+        }
+        const uint2 p = *reinterpret_cast<const uint2 *>(x + oa), q = *reinterpret_cast<const uint2 *>(x + ob);
+        if (FORM == kPairs) {
+            r.a[0] = make_float2(bf_lo(p.x), bf_lo(p.y));
+            r.b[0] = make_float2(bf_hi(p.x), bf_hi(p.y));
+            r.a[1] = make_float2(bf_lo(q.x), bf_lo(q.y));
+            r.b[1] = make_float2(bf_hi(q.x), bf_hi(q.y));
+        } else {
+            r.a[0] = make_float2(bf_lo(p.x), bf_hi(p.x));
+            r.a[1] = make_float2(bf_lo(p.y), bf_hi(p.y));
+            r.b[0] = make_float2(bf_lo(q.x), bf_hi(q.x));
+            r.b[1] = make_float2(bf_lo(q.y), bf_hi(q.y));
+        }
+        return r;
     }
-    __device__ __forceinline__ static int pb(const RopeArgs &a, int p) {
-        const int half = a.rot >> 1;
-        return a.interleaved ? 2 * p + 1 : p < half ? p + half : 2 * p + 1;
+    __device__ __forceinline__ void store(uint16_t *y, const Lane8 &r) const {
+        if (FORM == kSingles) {
+            const float f[8] = {r.a[0].x, r.a[0].y, r.a[1].x, r.a[1].y, r.b[0].x, r.b[0].y, r.b[1].x, r.b[1].y};
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                y[ca[u]] = (uint16_t)bf_pack(f[u], 0.0f);
+                y[cb[u]] = (uint16_t)bf_pack(f[4 + u], 0.0f);
+            }
+        } else if (FORM == kPairs) {
+            *reinterpret_cast<uint2 *>(y + oa) = make_uint2(bf_pack(r.a[0].x, r.b[0].x), bf_pack(r.a[0].y, r.b[0].y));
+            *reinterpret_cast<uint2 *>(y + ob) = make_uint2(bf_pack(r.a[1].x, r.b[1].x), bf_pack(r.a[1].y, r.b[1].y));
+        } else {
+            *reinterpret_cast<uint2 *>(y + oa) = make_uint2(bf_pack(r.a[0].x, r.a[0].y), bf_pack(r.a[1].x, r.a[1].y));
+            *reinterpret_cast<uint2 *>(y + ob) = make_uint2(bf_pack(r.b[0].x, r.b[0].y), bf_pack(r.b[1].x, r.b[1].y));
+        }
     }
 };
 
-template <bool VEC>
+template <int FORM>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
     const int j = threadIdx.x & 15;
+    const unsigned mine = 0xFFFFu << (threadIdx.x & 16);   // the half-warp: its two may walk different heads
     const int64_t unit = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> 4;
-    int64_t tok;
-    int part;
-    if (a.splits == 1) {
-        tok = unit;
-        part = 0;
-    } else {
-        tok = unit / a.splits;
-        part = (int)(unit - tok * a.splits);
-    }
-    // both half-warps of a warp take part in the shuffles; one past the end does nothing else
-    const bool live = tok < a.tokens;
-    PairMap<VEC> map;
+    const int64_t tok = a.splits == 1 ? unit : unit / a.splits;
+    const int part = a.splits == 1 ? 0 : (int)(unit - tok * a.splits);
+    if (tok >= a.tokens) return;
+    LaneMap<FORM> map;
     map.init(a, j);
-    float c[4], s[4];
-    const double pos = live ? (double)(a.pos ? a.pos[tok] : a.pos0 + tok) : 0.0;
+    float2 c[2], s[2];
+    {
+        const double pos = (double)(a.pos ? a.pos[tok] : a.pos0 + tok);
+        float cc[4], ss[4];
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
-        const int p = PairMap<VEC>::pair(j, u);
-        c[u] = 1.0f;
-        s[u] = 0.0f;
-        if (2 * p < a.rot) {
-            const double turns = pos * a.inv_freq[p] * 0.15915494309189533577;   // 1 / (2 pi)
-            sincospif((float)(2.0 * (turns - rint(turns))), &s[u], &c[u]);
+        for (int u = 0; u < 4; u++) {
+            const int p = pair_of<FORM>(j, u);
+            cc[u] = 1.0f;
+            ss[u] = 0.0f;
+            if (2 * p < a.rot) {
+                const double turns = pos * a.inv_freq[p] * 0.15915494309189533577;   // 1 / (2 pi)
+                sincospif((float)(2.0 * (turns - rint(turns))), &ss[u], &cc[u]);
+            }
         }
+        c[0] = make_float2(cc[0], cc[1]);
+        c[1] = make_float2(cc[2], cc[3]);
+        s[0] = make_float2(ss[0], ss[1]);
+        s[1] = make_float2(ss[2], ss[3]);
     }
-    const int hall = a.side[0].heads + a.side[1].heads;
-    const int h0 = part * a.per_split, h1 = min(hall, h0 + a.per_split);
-    for (int h = h0; h < h0 + a.per_split; h += kRopeUnroll) {
-        float va[kRopeUnroll][4], vb[kRopeUnroll][4];
+    const int all = a.side[0].heads + a.side[1].heads;
+    const int h0 = part * a.per_split, h1 = min(all, h0 + a.per_split);
+#pragma unroll 1
+    for (int which = 0; which < 2; which++) {
+        const RopeSide &sd = a.side[which];
+        const int first = which ? a.side[0].heads : 0;
+        const int lo = max(h0 - first, 0), hi = min(h1 - first, sd.heads);
+        if (lo >= hi) continue;
+        const uint16_t *x = sd.x + tok * sd.ld_tok;
+        uint16_t *y = sd.y + tok * sd.out_tok;
+        Lane8 w;
+        const float2 one = make_float2(1.0f, 1.0f);
+        w.a[0] = w.a[1] = w.b[0] = w.b[1] = one;
+        if (a.norm && sd.w) w = map.load(sd.w);
+        for (int h = lo; h < hi; h += kRopeUnroll) {
+            Lane8 v[kRopeUnroll];
 #pragma unroll
-        for (int n = 0; n < kRopeUnroll; n++) {
-            const bool on = live && h + n < h1;
-            const int which = h + n < a.side[0].heads ? 0 : 1;
-            const RopeSide &sd = a.side[which];
-            const int hh = h + n - (which ? a.side[0].heads : 0);
-            const uint16_t *x = sd.x + tok * sd.ld_tok + (int64_t)hh * sd.ld_head;
-            if (VEC) {
-                uint2 ra = make_uint2(0u, 0u), rb = ra;
-                if (on) {
-                    ra = *reinterpret_cast<const uint2 *>(x + map.oa);
-                    rb = *reinterpret_cast<const uint2 *>(x + map.ob);
+            for (int n = 0; n < kRopeUnroll; n++)   // past the last: the last again, not stored
+                v[n] = map.load(x + (int64_t)min(h + n, hi - 1) * sd.ld_head);
+            if (a.norm) {
+                float ss[kRopeUnroll];
+#pragma unroll
+                for (int n = 0; n < kRopeUnroll; n++) {
+                    float2 q = f2_mul(v[n].a[0], v[n].a[0]);
+                    q = f2_fma(v[n].a[1], v[n].a[1], q);
+                    q = f2_fma(v[n].b[0], v[n].b[0], q);
+                    q = f2_fma(v[n].b[1], v[n].b[1], q);
+                    ss[n] = __fadd_rn(q.x, q.y);
                 }
-                const float f[8] = {bf_lo(ra.x), bf_hi(ra.x), bf_lo(ra.y), bf_hi(ra.y),
-                                    bf_lo(rb.x), bf_hi(rb.x), bf_lo(rb.y), bf_hi(rb.y)};
 #pragma unroll
-                for (int u = 0; u < 4; u++) {
-                    va[n][u] = a.interleaved ? f[2 * u] : f[u];
-                    vb[n][u] = a.interleaved ? f[2 * u + 1] : f[4 + u];
-                }
-            } else {
+                for (int m = 1; m <= 8; m <<= 1)
 #pragma unroll
-                for (int u = 0; u < 4; u++) {
-                    const int p = PairMap<VEC>::pair(j, u);
-                    va[n][u] = on ? __uint_as_float((uint32_t)x[PairMap<VEC>::pa(a, p)] << 16) : 0.0f;
-                    vb[n][u] = on ? __uint_as_float((uint32_t)x[PairMap<VEC>::pb(a, p)] << 16) : 0.0f;
-                }
-            }
-        }
-        if (a.norm) {
-            float ss[kRopeUnroll];
+                    for (int n = 0; n < kRopeUnroll; n++) ss[n] = __fadd_rn(ss[n], __shfl_xor_sync(mine, ss[n], m));
 #pragma unroll
-            for (int n = 0; n < kRopeUnroll; n++) {
-                ss[n] = 0.0f;
+                for (int n = 0; n < kRopeUnroll; n++) {
+                    const float r = rsqrtf(__fmaf_rn(ss[n], 1.0f / 128.0f, a.eps));
+                    const float2 r2 = make_float2(r, r);
 #pragma unroll
-                for (int u = 0; u < 4; u++) ss[n] = __fmaf_rn(vb[n][u], vb[n][u], __fmaf_rn(va[n][u], va[n][u], ss[n]));
-            }
-#pragma unroll
-            for (int m = 1; m <= 8; m <<= 1)
-#pragma unroll
-                for (int n = 0; n < kRopeUnroll; n++)
-                    ss[n] = __fadd_rn(ss[n], __shfl_xor_sync(0xffffffffu, ss[n], m));
-#pragma unroll
-            for (int n = 0; n < kRopeUnroll; n++) {
-                const float r = rsqrtf(__fmaf_rn(ss[n], 1.0f / 128.0f, a.eps));
-                const uint16_t *w = a.side[h + n < a.side[0].heads ? 0 : 1].w;
-#pragma unroll
-                for (int u = 0; u < 4; u++) {
-                    const int p = PairMap<VEC>::pair(j, u);
-                    const int ia = VEC ? (a.interleaved ? map.oa + 2 * u : map.oa + u) : PairMap<VEC>::pa(a, p);
-                    const int ib = VEC ? (a.interleaved ? map.oa + 2 * u + 1 : map.ob + u) : PairMap<VEC>::pb(a, p);
-                    va[n][u] = __fmul_rn(va[n][u], r);
-                    vb[n][u] = __fmul_rn(vb[n][u], r);
-                    if (w) {
-                        va[n][u] = __fmul_rn(va[n][u], __uint_as_float((uint32_t)__ldg(w + ia) << 16));
-                        vb[n][u] = __fmul_rn(vb[n][u], __uint_as_float((uint32_t)__ldg(w + ib) << 16));
+                    for (int i = 0; i < 2; i++) {
+                        v[n].a[i] = f2_mul(f2_mul(v[n].a[i], r2), w.a[i]);
+                        v[n].b[i] = f2_mul(f2_mul(v[n].b[i], r2), w.b[i]);
                     }
                 }
             }
-        }
 #pragma unroll
-        for (int n = 0; n < kRopeUnroll; n++) {
-            if (!(live && h + n < h1)) continue;
-            const int which = h + n < a.side[0].heads ? 0 : 1;
-            const RopeSide &sd = a.side[which];
-            const int hh = h + n - (which ? a.side[0].heads : 0);
-            uint16_t *y = sd.y + tok * sd.out_tok + (int64_t)hh * sd.out_head;
-            float ya[4], yb[4];
+            for (int n = 0; n < kRopeUnroll; n++) {
+                Lane8 o;
 #pragma unroll
-            for (int u = 0; u < 4; u++) {
-                ya[u] = __fmaf_rn(va[n][u], c[u], -__fmul_rn(vb[n][u], s[u]));
-                yb[u] = __fmaf_rn(vb[n][u], c[u], __fmul_rn(va[n][u], s[u]));
-            }
-            if (VEC) {
-                uint2 ra, rb;
-                if (a.interleaved) {
-                    ra = make_uint2(bf_pack(ya[0], yb[0]), bf_pack(ya[1], yb[1]));
-                    rb = make_uint2(bf_pack(ya[2], yb[2]), bf_pack(ya[3], yb[3]));
-                } else {
-                    ra = make_uint2(bf_pack(ya[0], ya[1]), bf_pack(ya[2], ya[3]));
-                    rb = make_uint2(bf_pack(yb[0], yb[1]), bf_pack(yb[2], yb[3]));
+                for (int i = 0; i < 2; i++) {
+                    const float2 bs = f2_mul(v[n].b[i], s[i]), as = f2_mul(v[n].a[i], s[i]);
+                    o.a[i] = f2_fma(v[n].a[i], c[i], make_float2(-bs.x, -bs.y));
+                    o.b[i] = f2_fma(v[n].b[i], c[i], as);
                 }
-                *reinterpret_cast<uint2 *>(y + map.oa) = ra;
-                *reinterpret_cast<uint2 *>(y + map.ob) = rb;
-            } else {
-#pragma unroll
-                for (int u = 0; u < 4; u++) {
-                    const int p = PairMap<VEC>::pair(j, u);
-                    y[PairMap<VEC>::pa(a, p)] = (uint16_t)bf_pack(ya[u], 0.0f);
-                    y[PairMap<VEC>::pb(a, p)] = (uint16_t)bf_pack(yb[u], 0.0f);
-                }
+                if (h + n < hi) map.store(y + (int64_t)(h + n) * sd.out_head, o);
             }
         }
     }
@@ -274,9 +285,11 @@ extern "C" int hq_qk_norm_rope(const void *q, int64_t q_ld_token, int64_t q_ld_h
     const int64_t units = tokens * a.splits, per_cta = kRopeThreads / 16;
     const int64_t grid = (units + per_cta - 1) / per_cta;
     cudaStream_t s = (cudaStream_t)cuda_stream;
-    if (a.rot % 8 == 0)
-        norm_rope_kernel<true><<<(unsigned)grid, kRopeThreads, 0, s>>>(a);
+    if (a.rot % 8 != 0)
+        norm_rope_kernel<kSingles><<<(unsigned)grid, kRopeThreads, 0, s>>>(a);
+    else if (a.interleaved)
+        norm_rope_kernel<kPairs><<<(unsigned)grid, kRopeThreads, 0, s>>>(a);
     else
-        norm_rope_kernel<false><<<(unsigned)grid, kRopeThreads, 0, s>>>(a);
+        norm_rope_kernel<kHalves><<<(unsigned)grid, kRopeThreads, 0, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? HQ_OK : HQ_ECUDA;
 }
