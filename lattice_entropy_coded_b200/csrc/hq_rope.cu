@@ -136,7 +136,7 @@ struct LaneMap {
 };
 
 template <int FORM>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, FORM == kSingles ? 2 : 4) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
     const int j = threadIdx.x & 15;
     const unsigned mine = 0xFFFFu << (threadIdx.x & 16);   // the half-warp: its two may walk different heads
     const int64_t unit = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> 4;
