@@ -13,34 +13,39 @@ namespace hq {
 namespace {
 
 constexpr int kCombineWarps = 8;
+constexpr int kCombineSpread = 512;   // rows of all heads up to which a CTA's warps share one row
 
-// One warp per query row: the splits' sums rescaled to a common maximum and added, turned back
-// (D H_128, or Q^T), the visible drafts added, divided by the sum of all weights.
+// A query row: the splits' sums rescaled to a common maximum and added, turned back (D H_128, or Q^T),
+// the visible drafts added, divided by the sum of all weights.  Bound by the latency of its loads (a few
+// MB from L2): every warp asks for eight splits at a time, and with few rows (W = 8) the eight warps of
+// a CTA share one row, else (W = 1) each has its own.
+template <int W>
 __global__ void __launch_bounds__(kCombineWarps * 32) attention_combine(const __grid_constant__ AttnArgs a) {
+    constexpr int RPC = kCombineWarps / W;   // rows of a CTA
     __shared__ uint32_t sign[4];
-    __shared__ float xs[kCombineWarps][128];
-    __shared__ float ps[kCombineWarps][kAttnMaxQueries];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float4 xs[kCombineWarps][32];
+    __shared__ float ls[kCombineWarps];
+    __shared__ float ps[RPC][kAttnMaxQueries];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W;
     build_sign_table(sign, 1, a.seed[1]);
-    __syncthreads();
-    const int row = blockIdx.x * kCombineWarps + warp, head = blockIdx.y;
-    if (row >= a.rows) return;
-    const int qi = row / a.group, qh = head * a.group + row - qi * a.group;
+    const int row = blockIdx.x * RPC + warp / W, head = blockIdx.y;
+    const bool on = row < a.rows;
+    const int qi = on ? row / a.group : 0, qh = head * a.group + row - qi * a.group;
+    const int64_t d_head = head * a.d_ld_head + 4 * lane;
 
-    // drafts: log2 weights of two per lane
-    float m = kNegInf, sd[2] = {kNegInf, kNegInf};
+    // drafts: log2 weights (none for one that the row does not see)
     unsigned long long mine = 0;
-    if (a.mask) {
+    if (a.mask && on) {
         const unsigned long long all = a.n_q < 64 ? (1ull << a.n_q) - 1ull : ~0ull;
         mine = a.mask[qi] & all;
         const int64_t pos = a.len - 1 + __popcll(mine);
         const uint2 qr = *reinterpret_cast<const uint2 *>(a.q + qi * a.q_ld_tok + qh * a.q_ld_head + 4 * lane);
         const float q[4] = {__uint_as_float(qr.x << 16), __uint_as_float(qr.x & 0xFFFF0000u),
                             __uint_as_float(qr.y << 16), __uint_as_float(qr.y & 0xFFFF0000u)};
-        for (int j = 0; j < a.n_q; j++) {
-            float s = 0.0f;
+        for (int j = part; j < a.n_q; j += W) {
+            float s = kNegInf;
             if ((mine >> j) & 1ull) {
-                const uint2 kr = *reinterpret_cast<const uint2 *>(a.kd + j * a.d_ld_tok + head * a.d_ld_head + 4 * lane);
+                const uint2 kr = *reinterpret_cast<const uint2 *>(a.kd + j * a.d_ld_tok + d_head);
                 s = __fmul_rn(q[0], __uint_as_float(kr.x << 16));
                 s = __fmaf_rn(q[1], __uint_as_float(kr.x & 0xFFFF0000u), s);
                 s = __fmaf_rn(q[2], __uint_as_float(kr.y << 16), s);
@@ -50,40 +55,81 @@ __global__ void __launch_bounds__(kCombineWarps * 32) attention_combine(const __
                 const int64_t t = a.len - 1 + __popcll(a.mask[j] & all);
                 // a draft later than the query, or outside its window, is not visible whatever the mask says
                 const bool see = t <= pos && (a.window <= 0 || t > pos - a.window || t < a.sinks);
-                if ((j & 31) == lane) sd[j >> 5] = see ? __fmul_rn(s, a.scale_log2) : kNegInf;
+                s = see ? __fmul_rn(s, a.scale_log2) : kNegInf;
+            }
+            if (lane == 0) ps[warp / W][j] = s;
+        }
+    }
+    // what the splits left
+    cudaGridDependencySynchronize();
+    const int64_t step = (int64_t)a.heads * a.row_pad, at = (int64_t)head * a.row_pad + row;
+    float m = kNegInf;
+    if (on)
+        for (int sp = lane; sp < a.splits; sp += 32) m = fmaxf(m, a.ml[sp * step + at].x);
+    __syncthreads();   // the drafts' weights and the signs are there
+    if (mine)
+        for (int j = lane; j < a.n_q; j += 32) m = fmaxf(m, ps[warp / W][j]);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == kNegInf ? 0.0f : m;
+    float l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (on) {
+        // this warp's splits part, part + W, ...: weights by lane, then their sums
+        for (int s0 = 0; s0 < a.splits; s0 += 32 * W) {
+            const int sp = s0 + lane * W + part;
+            float f = 0.0f;
+            if (sp < a.splits) {
+                const float2 ml = a.ml[sp * step + at];
+                f = ml.y == 0.0f ? 0.0f : ex2(__fsub_rn(ml.x, base));   // 0: the split saw nothing of this row
+                l = __fmaf_rn(ml.y, f, l);
+            }
+            const int n = min(32, (a.splits - s0 - part + W - 1) / W);
+            for (int i0 = 0; i0 < n; i0 += 8) {
+                float4 x[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    x[i] = i0 + i < n ? *reinterpret_cast<const float4 *>(
+                                            a.part + ((s0 + (i0 + i) * W + part) * step + at) * kTile + 4 * lane)
+                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float fi = __shfl_sync(0xffffffffu, f, (i0 + i) & 31);
+                    o.x = __fmaf_rn(x[i].x, fi, o.x);
+                    o.y = __fmaf_rn(x[i].y, fi, o.y);
+                    o.z = __fmaf_rn(x[i].z, fi, o.z);
+                    o.w = __fmaf_rn(x[i].w, fi, o.w);
+                }
             }
         }
-        m = fmaxf(sd[0], sd[1]);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int s = 1; s < 32; s <<= 1) l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, s));
     }
-    // splits
-    const int64_t step = (int64_t)a.heads * a.row_pad, at = (int64_t)head * a.row_pad + row;
-    float top = kNegInf;
-    for (int sp = lane; sp < a.splits; sp += 32) top = fmaxf(top, a.ml[sp * step + at].x);
+    if (W > 1) {
+        xs[warp][lane] = o;
+        if (lane == 0) ls[warp] = l;
+        __syncthreads();
+        if (part) return;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    m = fmaxf(m, top);
-    const float base = m == kNegInf ? 0.0f : m;
-    float l = 0.0f, o4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int sp = 0; sp < a.splits; sp++) {
-        const float2 ml = a.ml[sp * step + at];
-        if (ml.y == 0.0f) continue;   // the split saw nothing of this row
-        const float f = ex2(__fsub_rn(ml.x, base));
-        const float4 x = *reinterpret_cast<const float4 *>(a.part + (sp * step + at) * kTile + 4 * lane);
-        l = __fmaf_rn(ml.y, f, l);
-        o4[0] = __fmaf_rn(x.x, f, o4[0]);
-        o4[1] = __fmaf_rn(x.y, f, o4[1]);
-        o4[2] = __fmaf_rn(x.z, f, o4[2]);
-        o4[3] = __fmaf_rn(x.w, f, o4[3]);
+        for (int i = 1; i < W; i++) {
+            const float4 x = xs[warp + i][lane];
+            o.x = __fadd_rn(o.x, x.x);
+            o.y = __fadd_rn(o.y, x.y);
+            o.z = __fadd_rn(o.z, x.z);
+            o.w = __fadd_rn(o.w, x.w);
+            l = __fadd_rn(l, ls[warp + i]);
+        }
     }
+    if (!on) return;
     // back from the rotated domain
+    float o4[4] = {o.x, o.y, o.z, o.w};
     if (a.rot[1]) {
-        reinterpret_cast<float4 *>(xs[warp])[lane] = make_float4(o4[0], o4[1], o4[2], o4[3]);
+        xs[warp][lane] = o;
         __syncwarp();
         o4[0] = o4[1] = o4[2] = o4[3] = 0.0f;
+#pragma unroll 8
         for (int i = 0; i < 128; i++) {
-            const float z = xs[warp][i];
+            const float z = reinterpret_cast<const float *>(xs[warp])[i];
             const float4 q = __ldg(reinterpret_cast<const float4 *>(a.rot[1] + i * 128) + lane);
             o4[0] = __fmaf_rn(q.x, z, o4[0]);
             o4[1] = __fmaf_rn(q.y, z, o4[1]);
@@ -99,25 +145,17 @@ __global__ void __launch_bounds__(kCombineWarps * 32) attention_combine(const __
             if ((e >> ((c >> 1) + 16 * (c & 1))) & 1u) o4[i] = -o4[i];
         }
     }
-    if (mine) {
-        const float p0 = ex2(__fsub_rn(sd[0], base)), p1 = ex2(__fsub_rn(sd[1], base));
-        ps[warp][lane] = p0;
-        ps[warp][lane + 32] = p1;
-        float pl = __fadd_rn(p0, p1);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) pl = __fadd_rn(pl, __shfl_xor_sync(0xffffffffu, pl, o));
-        l = __fadd_rn(l, pl);
-        __syncwarp();
-        for (int j = 0; j < a.n_q; j++) {
-            const float p = ps[warp][j];
-            // a draft that the row does not see may hold anything
-            if (p == 0.0f) continue;
-            const uint2 vr = *reinterpret_cast<const uint2 *>(a.vd + j * a.d_ld_tok + head * a.d_ld_head + 4 * lane);
-            o4[0] = __fmaf_rn(p, __uint_as_float(vr.x << 16), o4[0]);
-            o4[1] = __fmaf_rn(p, __uint_as_float(vr.x & 0xFFFF0000u), o4[1]);
-            o4[2] = __fmaf_rn(p, __uint_as_float(vr.y << 16), o4[2]);
-            o4[3] = __fmaf_rn(p, __uint_as_float(vr.y & 0xFFFF0000u), o4[3]);
-        }
+    for (unsigned long long left = mine; left; left &= left - 1) {
+        const int j = __ffsll((long long)left) - 1;
+        const float p = ex2(__fsub_rn(ps[warp / W][j], base));
+        // a draft that the row does not see may hold anything
+        if (p == 0.0f) continue;
+        l = __fadd_rn(l, p);
+        const uint2 vr = *reinterpret_cast<const uint2 *>(a.vd + j * a.d_ld_tok + d_head);
+        o4[0] = __fmaf_rn(p, __uint_as_float(vr.x << 16), o4[0]);
+        o4[1] = __fmaf_rn(p, __uint_as_float(vr.x & 0xFFFF0000u), o4[1]);
+        o4[2] = __fmaf_rn(p, __uint_as_float(vr.y << 16), o4[2]);
+        o4[3] = __fmaf_rn(p, __uint_as_float(vr.y & 0xFFFF0000u), o4[3]);
     }
     const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);   // a row that sees nothing: zeros
 #pragma unroll
@@ -133,6 +171,21 @@ __global__ void __launch_bounds__(kCombineWarps * 32) attention_combine(const __
     if (a.lse && lane == 0)
         a.lse[(int64_t)qi * a.heads * a.group + qh] =
             l == 0.0f ? kNegInf : __fmul_rn(__fadd_rn(m, log2f(l)), 0.69314718055994530942f);
+}
+
+// The combine may start while the splits run: its own inputs come first, and it waits for theirs.
+template <int W>
+cudaError_t launch_combine(const AttnArgs &a, cudaStream_t s) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)((a.rows + kCombineWarps / W - 1) / (kCombineWarps / W)), (unsigned)a.heads);
+    c.blockDim = dim3(kCombineWarps * 32);
+    c.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = at;
+    c.numAttrs = a.splits ? 1 : 0;
+    return cudaLaunchKernelEx(&c, attention_combine<W>, a);
 }
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -229,9 +282,8 @@ int attend(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *sp, c
         a.ml = (float2 *)(a.part + (size_t)a.splits * a.heads * a.row_pad * kTile);
         if (launch_attention(k->params.lattice, k->params.dither, a, s) != cudaSuccess) return HQ_ECUDA;
     }
-    const dim3 g((unsigned)((a.rows + kCombineWarps - 1) / kCombineWarps), (unsigned)a.heads);
-    attention_combine<<<g, kCombineWarps * 32, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? HQ_OK : HQ_ECUDA;
+    const bool spread = (int64_t)a.rows * a.heads <= kCombineSpread;
+    return (spread ? launch_combine<kCombineWarps>(a, s) : launch_combine<1>(a, s)) == cudaSuccess ? HQ_OK : HQ_ECUDA;
 }
 
 }  // namespace
