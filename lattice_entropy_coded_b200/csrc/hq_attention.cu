@@ -33,31 +33,56 @@ __global__ void __launch_bounds__(kCombineWarps * 32) attention_combine(const __
     const int qi = on ? row / a.group : 0, qh = head * a.group + row - qi * a.group;
     const int64_t d_head = head * a.d_ld_head + 4 * lane;
 
-    // drafts: log2 weights (none for one that the row does not see)
+    // drafts that the row sees (one later than the query, or outside its window, is not visible whatever
+    // the mask says), and their log2 weights
     unsigned long long mine = 0;
     if (a.mask && on) {
-        const unsigned long long all = a.n_q < 64 ? (1ull << a.n_q) - 1ull : ~0ull;
-        mine = a.mask[qi] & all;
-        const int64_t pos = a.len - 1 + __popcll(mine);
+        const unsigned long long all = a.n_q < 64 ? (1ull << a.n_q) - 1ull : ~0ull, given = a.mask[qi] & all;
+        const int64_t pos = a.len - 1 + __popcll(given);
+        unsigned half[2];
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            const int j = lane + 32 * u;
+            bool see = ((given >> j) & 1ull) != 0ull;
+            if (see) {
+                const int64_t t = a.len - 1 + __popcll(a.mask[j] & all);
+                see = t <= pos && (a.window <= 0 || t > pos - a.window || t < a.sinks);
+            }
+            half[u] = __ballot_sync(0xffffffffu, see);
+        }
+        mine = (unsigned long long)half[1] << 32 | half[0];
         const uint2 qr = *reinterpret_cast<const uint2 *>(a.q + qi * a.q_ld_tok + qh * a.q_ld_head + 4 * lane);
         const float q[4] = {__uint_as_float(qr.x << 16), __uint_as_float(qr.x & 0xFFFF0000u),
                             __uint_as_float(qr.y << 16), __uint_as_float(qr.y & 0xFFFF0000u)};
-        for (int j = part; j < a.n_q; j += W) {
-            float s = kNegInf;
-            if ((mine >> j) & 1ull) {
-                const uint2 kr = *reinterpret_cast<const uint2 *>(a.kd + j * a.d_ld_tok + d_head);
-                s = __fmul_rn(q[0], __uint_as_float(kr.x << 16));
-                s = __fmaf_rn(q[1], __uint_as_float(kr.x & 0xFFFF0000u), s);
-                s = __fmaf_rn(q[2], __uint_as_float(kr.y << 16), s);
-                s = __fmaf_rn(q[3], __uint_as_float(kr.y & 0xFFFF0000u), s);
+        // four at a time; the warps of a row take turns
+        int turn = 0;
+        for (unsigned long long left = mine; left; turn++) {
+            int j[4];
+            uint2 kr[4];
+            float s[4];
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
-                const int64_t t = a.len - 1 + __popcll(a.mask[j] & all);
-                // a draft later than the query, or outside its window, is not visible whatever the mask says
-                const bool see = t <= pos && (a.window <= 0 || t > pos - a.window || t < a.sinks);
-                s = see ? __fmul_rn(s, a.scale_log2) : kNegInf;
+            for (int i = 0; i < 4; i++) {
+                j[i] = left ? __ffsll((long long)left) - 1 : -1;
+                left &= left - 1;
             }
-            if (lane == 0) ps[warp / W][j] = s;
+            if (turn % W != part) continue;
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                kr[i] = j[i] >= 0 ? *reinterpret_cast<const uint2 *>(a.kd + j[i] * a.d_ld_tok + d_head) : make_uint2(0u, 0u);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                s[i] = __fmul_rn(q[0], __uint_as_float(kr[i].x << 16));
+                s[i] = __fmaf_rn(q[1], __uint_as_float(kr[i].x & 0xFFFF0000u), s[i]);
+                s[i] = __fmaf_rn(q[2], __uint_as_float(kr[i].y << 16), s[i]);
+                s[i] = __fmaf_rn(q[3], __uint_as_float(kr[i].y & 0xFFFF0000u), s[i]);
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+                for (int i = 0; i < 4; i++) s[i] = __fadd_rn(s[i], __shfl_xor_sync(0xffffffffu, s[i], o));
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (lane == 0 && j[i] >= 0) ps[warp / W][j[i]] = __fmul_rn(s[i], a.scale_log2);
         }
     }
     // what the splits left
@@ -68,7 +93,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) attention_combine(const __
         for (int sp = lane; sp < a.splits; sp += 32) m = fmaxf(m, a.ml[sp * step + at].x);
     __syncthreads();   // the drafts' weights and the signs are there
     if (mine)
-        for (int j = lane; j < a.n_q; j += 32) m = fmaxf(m, ps[warp / W][j]);
+        for (int j = lane; j < a.n_q; j += 32)
+            if ((mine >> j) & 1ull) m = fmaxf(m, ps[warp / W][j]);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float base = m == kNegInf ? 0.0f : m;
@@ -145,17 +171,27 @@ __global__ void __launch_bounds__(kCombineWarps * 32) attention_combine(const __
             if ((e >> ((c >> 1) + 16 * (c & 1))) & 1u) o4[i] = -o4[i];
         }
     }
-    for (unsigned long long left = mine; left; left &= left - 1) {
-        const int j = __ffsll((long long)left) - 1;
-        const float p = ex2(__fsub_rn(ps[warp / W][j], base));
-        // a draft that the row does not see may hold anything
-        if (p == 0.0f) continue;
-        l = __fadd_rn(l, p);
-        const uint2 vr = *reinterpret_cast<const uint2 *>(a.vd + j * a.d_ld_tok + d_head);
-        o4[0] = __fmaf_rn(p, __uint_as_float(vr.x << 16), o4[0]);
-        o4[1] = __fmaf_rn(p, __uint_as_float(vr.x & 0xFFFF0000u), o4[1]);
-        o4[2] = __fmaf_rn(p, __uint_as_float(vr.y << 16), o4[2]);
-        o4[3] = __fmaf_rn(p, __uint_as_float(vr.y & 0xFFFF0000u), o4[3]);
+    // what an invisible draft holds does not matter: only those of `mine` are read
+    for (unsigned long long left = mine; left;) {
+        int j[4];
+        uint2 vr[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            j[i] = left ? __ffsll((long long)left) - 1 : -1;
+            left &= left - 1;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            vr[i] = j[i] >= 0 ? *reinterpret_cast<const uint2 *>(a.vd + j[i] * a.d_ld_tok + d_head) : make_uint2(0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float p = j[i] >= 0 ? ex2(__fsub_rn(ps[warp / W][j[i] < 0 ? 0 : j[i]], base)) : 0.0f;
+            l = __fadd_rn(l, p);
+            o4[0] = __fmaf_rn(p, __uint_as_float(vr[i].x << 16), o4[0]);
+            o4[1] = __fmaf_rn(p, __uint_as_float(vr[i].x & 0xFFFF0000u), o4[1]);
+            o4[2] = __fmaf_rn(p, __uint_as_float(vr[i].y << 16), o4[2]);
+            o4[3] = __fmaf_rn(p, __uint_as_float(vr[i].y & 0xFFFF0000u), o4[3]);
+        }
     }
     const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);   // a row that sees nothing: zeros
 #pragma unroll
@@ -274,7 +310,9 @@ int attend(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *sp, c
         uint64_t per_head = k->chunks / (uint64_t)k->heads;
         if (a.window > 0) {
             const uint64_t w = (uint64_t)(a.window + sp->n_q + a.sinks) + 4;
-            if (w < per_head) per_head = w;
+            // at the cache's average of tokens to a chunk (only the split depends on it)
+            const uint64_t c = w * per_head / (uint64_t)(k->tokens > 0 ? k->tokens : 1) + 2;
+            if (c < per_head) per_head = c;
         }
         a.splits = attn_splits(a.heads, a.rows, per_head);
         a.short_steps = attn_short(a.heads, a.rows, per_head);

@@ -77,9 +77,9 @@ cudaError_t launch_attention_e8(int dither, const AttnArgs &a, cudaStream_t s);
 constexpr int kNarrowRows = 16;
 inline int attn_row_pad(int rows) { return rows <= kNarrowRows ? 16 : (rows + 127) / 128 * 128; }
 // Whether steps are of one chunk, whose rounds four warps share, instead of a chunk to a warp: while
-// that still leaves at most one step to a CTA (short caches, where the time is that of one step).
+// that leaves at most two such steps to a CTA (short caches, where the time is that of one step).
 inline bool attn_short(int heads, int rows, uint64_t chunks_per_head) {
-    return rows <= kNarrowRows && (uint64_t)heads * chunks_per_head <= (uint64_t)kAttnCtas;
+    return rows <= kNarrowRows && (uint64_t)heads * chunks_per_head <= 2 * (uint64_t)kAttnCtas;
 }
 // Splits of the tokens: the CTAs of all heads and row blocks together fill the GPU once.
 inline int attn_splits(int heads, int rows, uint64_t chunks_per_head) {
@@ -135,29 +135,55 @@ __device__ __forceinline__ void load_row(const AttnArgs &a, uint64_t append, Att
     r.base = base;
     r.count = (uint64_t)(((int64_t)r.row.tokens + 31) / 32);
 }
-__device__ __forceinline__ void find_row(const AttnArgs &a, uint64_t i, AttnRow &r) {
+// The append table is searched through a sample of it in shared memory (all of it up to kTop appends):
+// one load's latency for the sample instead of one for every step of a search, which on a short cache
+// was most of the kernel's time.
+constexpr int kTop = 128;
+struct TopRow {
+    uint64_t first_chunk;
+    int64_t token0;
+};
+struct Table {
+    const AttnArgs &a;
+    const TopRow *top;
+    uint64_t stride, n;   // sample s is append s * stride
+    __device__ __forceinline__ Table(const AttnArgs &args, TopRow *t) : a(args), top(t) {
+        stride = (a.n_appends + kTop - 1) / kTop;
+        n = (a.n_appends + stride - 1) / stride;
+    }
+    // by the whole CTA; the caller synchronises
+    __device__ __forceinline__ void load(TopRow *t) const {
+        for (uint64_t i = threadIdx.x; i < n; i += blockDim.x)
+            t[i] = *reinterpret_cast<const TopRow *>(&a.table[0][i * stride]);
+    }
+    // the last append whose first chunk is at most x (by chunk), or whose first token is (else); 0 if none
+    template <bool CHUNK>
+    __device__ __forceinline__ uint64_t find(int64_t x) const {
+        uint64_t lo = 0, hi = n - 1;
+        while (lo < hi) {
+            const uint64_t mid = (lo + hi + 1) >> 1;
+            if ((CHUNK ? (int64_t)top[mid].first_chunk : top[mid].token0) <= x) lo = mid; else hi = mid - 1;
+        }
+        if (stride == 1) return lo;
+        lo *= stride;
+        hi = min(lo + stride, a.n_appends) - 1;
+        while (lo < hi) {
+            const uint64_t mid = (lo + hi + 1) >> 1;
+            if ((CHUNK ? (int64_t)a.table[0][mid].first_chunk : a.table[0][mid].token0) <= x) lo = mid; else hi = mid - 1;
+        }
+        return lo;
+    }
+    // the append of per-head chunk i
+    __device__ __forceinline__ uint64_t append_of(uint64_t i) const { return find<true>((int64_t)(i * (uint64_t)a.heads)); }
+};
+__device__ __forceinline__ void find_row(const Table &t, uint64_t i, AttnRow &r) {
     if (i >= r.base && i < r.base + r.count) return;
-    if (i >= r.base + r.count && r.append + 1 < a.n_appends) {
-        load_row(a, r.append + 1, r);
-        if (i >= r.base && i < r.base + r.count) return;
-    }
-    const uint64_t first = i * (uint64_t)a.heads;
-    uint64_t lo = 0, hi = a.n_appends - 1;
-    while (lo < hi) {
-        const uint64_t mid = (lo + hi + 1) >> 1;
-        if (a.table[0][mid].first_chunk <= first) lo = mid; else hi = mid - 1;
-    }
-    load_row(a, lo, r);
+    load_row(t.a, t.append_of(i), r);
 }
 // Per-head chunks that lie wholly before token t (round_up: that hold any token before t).
-__device__ __forceinline__ uint64_t chunks_before(const AttnArgs &a, int64_t t, bool round_up) {
-    uint64_t lo = 0, hi = a.n_appends - 1;
-    while (lo < hi) {
-        const uint64_t mid = (lo + hi + 1) >> 1;
-        if (a.table[0][mid].token0 <= t) lo = mid; else hi = mid - 1;
-    }
+__device__ __forceinline__ uint64_t chunks_before(const Table &tab, int64_t t, bool round_up) {
     AttnRow r;
-    load_row(a, lo, r);
+    load_row(tab.a, tab.find<false>(t), r);
     const int64_t in = t - r.row.token0;
     if (in <= 0) return r.base;
     const uint64_t n = (uint64_t)(round_up ? (in + 31) / 32 : in / 32);
@@ -278,9 +304,8 @@ __device__ __forceinline__ void e8_dither(uint64_t z0, float (&d)[8]) {
 }
 
 // ------------------------------------------------------------------ decode
-// Forms of the Rice code: no remainders at all (k = 0: the 2-bit caches), remainders read four
-// windows at a time (k <= 4, one parameter), or bit by bit.
-enum AttnForm { kFormUnary = 0, kFormWindows = 1, kFormGeneral = 2 };
+// Forms of the Rice code: no remainders at all (k = 0: the 2-bit caches), or any parameters.
+enum AttnForm { kFormUnary = 0, kFormGeneral = 1 };
 
 // Unary pairs of E8 at k = 0: the next 10 stream bits -> both codewords.  Bits 0..4 their length,
 // byte 1 and byte 2 the two codes 2 m + 128 (2 m the zigzag inverse doubled), bit 24 the parity of
@@ -296,127 +321,137 @@ __device__ __forceinline__ uint32_t pair_entry(uint32_t w) {
            (((a ^ b) >> 1) & 1u) << 24 | ((a >> 1) & 1u) << 25;
 }
 
-// The 32 codes (minus dither) of a lane's quarter of a tile, times `scale`, as 16 fp16 pairs.
+// What a lane decodes in a round: its quarter of a tile, 32 codes in four blocks of 8.
+struct Quarter {
+    const uint32_t *un, *rem;       // unary and remainder planes
+    uint32_t nu, nr;                // their words
+    uint32_t bp;                    // next unary bit
+    uint32_t rb;                    // next remainder bit
+    uint32_t coset;                 // E8: coset bits of the blocks left
+    unsigned long long e0;          // dither counter of the next element (E8: the pair's generator state)
+    bool ok;
+};
+template <int LAT, int FORM>
+__device__ __forceinline__ void open_quarter(Quarter &t, const uint32_t *src, uint32_t nc, uint32_t nr, uint32_t nu, int k,
+                                             int kl, uint64_t seed, uint32_t start, uint32_t segi,
+                                             unsigned long long e0) {
+    t.rem = src + nc;
+    t.un = src + nc + nr;
+    t.nu = nu;
+    t.nr = nr;
+    t.bp = start;
+    t.rb = FORM == kFormUnary ? 0u : segi * 4u * group_rem_bits<Lattice<LAT>::N>(k, kl);
+    t.coset = LAT == HQ_E8 ? src[segi >> 3] >> (4 * (segi & 7u)) : 0u;
+    t.e0 = e0 + 32ull * (segi & 3u);
+    if (LAT == HQ_E8) t.e0 = (seed ^ kDitherSalt) + ((t.e0 >> 1) + 1ull) * kSplitGolden;
+    t.ok = true;
+}
+
+// The next 8 codes (minus dither) times `scale`, as 4 fp16 pairs.
 template <int LAT, bool DITHER, int FORM, bool STAGED>
-__device__ __forceinline__ bool decode_quarter(const uint32_t *src, uint32_t nc, uint32_t nr, uint32_t nu, int k, int kl,
-                                               uint32_t bp, uint32_t segi, int q, unsigned long long e0, uint64_t seed,
-                                               float scale, const uint32_t *pairs, uint32_t (&w)[16]) {
+__device__ __forceinline__ void decode_block(Quarter &t, int k, int kl, uint64_t seed, float scale, const uint32_t *pairs,
+                                             uint32_t (&w)[4]) {
     using L = Lattice<LAT>;
     constexpr int N = L::N;
-    const uint32_t *un = src + nc + nr;
-    const uint32_t pk = 1u << k, pkl = 1u << kl;
-    const uint32_t gbits = group_rem_bits<N>(k, kl), lane_bits = 4u * gbits;
-    bool ok = true;
-    uint32_t rx[4] = {0u, 0u, 0u, 0u};
-    if (FORM == kFormWindows && k > 0) rem_windows(src + nc + segi * (uint32_t)k, k, rx);
-    const uint32_t cw = (LAT == HQ_E8) ? src[segi >> 3] : 0u;
-    const uint32_t coset = (cw >> (4 * (segi & 7u))) & 0xFu;
-    const float2 s2 = make_float2(scale, scale);
-    // E8 with dither: d comes in units of 2^-22
-    const float2 sd2 = make_float2(__fmul_rn(scale, -0x1p-22f), __fmul_rn(scale, -0x1p-22f));
-    const uint64_t z0 = (seed ^ kDitherSalt) + ((e0 >> 1) + (uint64_t)(16 * q) + 1ull) * kSplitGolden;
+    float u[8];
+    const uint32_t c = t.coset & 1u;
+    t.coset >>= 1;
+    if constexpr (LAT == HQ_E8 && FORM == kFormUnary && STAGED) {
+        // The plane's terminators were counted, so a lane's 32 codewords end inside it (or in the pad
+        // behind its last word, which the second word of a window may reach).
+        uint32_t e[4], used = 0;
 #pragma unroll
-    for (int g = 0; g < 4; g++) {
-        float u[8];
-        if constexpr (LAT == HQ_E8 && FORM == kFormUnary && STAGED) {
-            // The plane's terminators were counted, so a lane's 32 codewords end inside it (or in the pad
-            // behind its last word, which the second word of a window may reach).
-            const uint32_t c = (coset >> g) & 1u;
-            uint32_t e[4], used = 0;
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const uint32_t *p = un + ((bp + used) >> 5);
-                uint32_t x = __funnelshift_r(p[0], p[1], bp + used);
-                e[2 * h] = pairs[x & ((1u << kPairBits) - 1u)];
-                x = __funnelshift_r(x, 0u, e[2 * h]);
-                e[2 * h + 1] = pairs[x & ((1u << kPairBits) - 1u)];
-                used += (e[2 * h] + e[2 * h + 1]) & 0x1Fu;
-            }
-            if ((int32_t)(e[0] & e[1] & e[2] & e[3]) < 0) {
-                bp += used;
-                // the stripped parity of m_7: that of m_0 .. m_6
-                const uint32_t p7 = ((e[0] ^ e[1] ^ e[2]) >> 24 ^ e[3] >> 25) & 1u;
-                const float off = __fsub_rn((float)(int)c, 8388608.0f + 128.0f);
-                const float2 o2 = make_float2(off, off);
-#pragma unroll
-                for (int h = 0; h < 4; h++) {
-                    const float2 f = make_float2(__uint_as_float(__byte_perm(e[h], 0x4B000000u, 0x7441)),
-                                                 __uint_as_float(__byte_perm(e[h], 0x4B000000u, 0x7442)));
-                    const float2 r = f2_add(f, o2);
-                    u[2 * h] = r.x;
-                    u[2 * h + 1] = r.y;
-                }
-                // 2 (2 m_7 + p) + c from 2 m_7 + c
-                u[7] = __fadd_rn(__fadd_rn(u[7], u[7]), (float)((int)(2u * p7) - (int)c));
-            } else {
-                uint32_t zq[8];
-                unary4<STAGED>(un, nu, bp, ok, zq);
-                unary4<STAGED>(un, nu, bp, ok, zq + 4);
-                int32_t qq[8];
-                e8_codes_from_symbols(zq, c, qq);
-                decoded_point<HQ_E8>(qq, u);
-            }
-        } else {
-            uint32_t qv[8], rv[8];
-            unary4<STAGED>(un, nu, bp, ok, qv);
-            unary4<STAGED>(un, nu, bp, ok, qv + 4);
-            if (FORM == kFormGeneral) {
-                rem_group_mixed<N, STAGED>(src + nc, nr, segi * lane_bits, g, k, kl, gbits, rv);
-            } else if (FORM == kFormWindows) {
-                const uint32_t mask = (1u << k) - 1u;
-                uint32_t xw = rx[g];
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    rv[i] = xw & mask;
-                    xw >>= k;
-                }
-            }
-#pragma unroll
-            for (int bb = 0; bb < 8 / N; bb++) {
-                int32_t qq[N];
-                float p[N];
-                uint32_t zb[N];
-#pragma unroll
-                for (int i = 0; i < N; i++)
-                    zb[i] = FORM == kFormUnary ? qv[bb * N + i]
-                                               : imad(qv[bb * N + i], (N > 1 && i == N - 1) ? pkl : pk, rv[bb * N + i]);
-                if constexpr (LAT == HQ_E8) {
-                    e8_codes_from_symbols(zb, (coset >> g) & 1u, qq);
-                } else {
-                    int32_t m[N];
-#pragma unroll
-                    for (int i = 0; i < N; i++) m[i] = unzigzag(zb[i]);
-                    L::reinsert(m, 0u, qq);
-                }
-                decoded_point<LAT>(qq, p);
-                if (DITHER && LAT != HQ_E8) {
-                    float d[N];
-                    dither_block<LAT>(seed, e0 + (unsigned long long)(32 * q + 8 * g + bb * N), d);
-#pragma unroll
-                    for (int i = 0; i < N; i++) p[i] = __fsub_rn(p[i], d[i]);
-                }
-#pragma unroll
-                for (int i = 0; i < N; i++) u[bb * N + i] = p[i];
-            }
+        for (int h = 0; h < 2; h++) {
+            const uint32_t *p = t.un + ((t.bp + used) >> 5);
+            uint32_t x = __funnelshift_r(p[0], p[1], t.bp + used);
+            e[2 * h] = pairs[x & ((1u << kPairBits) - 1u)];
+            x = __funnelshift_r(x, 0u, e[2 * h]);
+            e[2 * h + 1] = pairs[x & ((1u << kPairBits) - 1u)];
+            used += (e[2 * h] + e[2 * h + 1]) & 0x1Fu;
         }
-        if constexpr (DITHER && LAT == HQ_E8) {
-            float d[8];
-            e8_dither(z0 + (uint64_t)(4 * g) * kSplitGolden, d);
+        if ((int32_t)(e[0] & e[1] & e[2] & e[3]) < 0) {
+            t.bp += used;
+            // the stripped parity of m_7: that of m_0 .. m_6
+            const uint32_t p7 = ((e[0] ^ e[1] ^ e[2]) >> 24 ^ e[3] >> 25) & 1u;
+            const float off = __fsub_rn((float)(int)c, 8388608.0f + 128.0f);
+            const float2 o2 = make_float2(off, off);
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const float2 x = f2_fma(make_float2(d[2 * j], d[2 * j + 1]), sd2, f2_mul(make_float2(u[2 * j], u[2 * j + 1]), s2));
-                w[4 * g + j] = h2_pack(x.x, x.y);
+            for (int h = 0; h < 4; h++) {
+                const float2 f = make_float2(__uint_as_float(__byte_perm(e[h], 0x4B000000u, 0x7441)),
+                                             __uint_as_float(__byte_perm(e[h], 0x4B000000u, 0x7442)));
+                const float2 r = f2_add(f, o2);
+                u[2 * h] = r.x;
+                u[2 * h + 1] = r.y;
             }
+            // 2 (2 m_7 + p) + c from 2 m_7 + c
+            u[7] = __fadd_rn(__fadd_rn(u[7], u[7]), (float)((int)(2u * p7) - (int)c));
         } else {
+            uint32_t zq[8];
+            unary4<STAGED>(t.un, t.nu, t.bp, t.ok, zq);
+            unary4<STAGED>(t.un, t.nu, t.bp, t.ok, zq + 4);
+            int32_t qq[8];
+            e8_codes_from_symbols(zq, c, qq);
+            decoded_point<HQ_E8>(qq, u);
+        }
+    } else {
+        uint32_t qv[8], rv[8];
+        unary4<STAGED>(t.un, t.nu, t.bp, t.ok, qv);
+        unary4<STAGED>(t.un, t.nu, t.bp, t.ok, qv + 4);
+        if (FORM == kFormGeneral) {
+            const uint32_t gbits = group_rem_bits<N>(k, kl);
+            rem_group_mixed<N, STAGED>(t.rem, t.nr, t.rb, 0, k, kl, gbits, rv);
+            t.rb += gbits;
+        }
+        const uint32_t pk = 1u << k, pkl = 1u << kl;
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const float2 x = f2_mul(make_float2(u[2 * j], u[2 * j + 1]), s2);
-                w[4 * g + j] = h2_pack(x.x, x.y);
+        for (int bb = 0; bb < 8 / N; bb++) {
+            int32_t qq[N];
+            float p[N];
+            uint32_t zb[N];
+#pragma unroll
+            for (int i = 0; i < N; i++)
+                zb[i] = FORM == kFormUnary ? qv[bb * N + i]
+                                           : imad(qv[bb * N + i], (N > 1 && i == N - 1) ? pkl : pk, rv[bb * N + i]);
+            if constexpr (LAT == HQ_E8) {
+                e8_codes_from_symbols(zb, c, qq);
+            } else {
+                int32_t m[N];
+#pragma unroll
+                for (int i = 0; i < N; i++) m[i] = unzigzag(zb[i]);
+                L::reinsert(m, 0u, qq);
             }
+            decoded_point<LAT>(qq, p);
+            if (DITHER && LAT != HQ_E8) {
+                float d[N];
+                dither_block<LAT>(seed, t.e0 + (unsigned long long)(bb * N), d);
+#pragma unroll
+                for (int i = 0; i < N; i++) p[i] = __fsub_rn(p[i], d[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < N; i++) u[bb * N + i] = p[i];
         }
     }
-    return ok && bp <= nu * 32u;
+    const float2 s2 = make_float2(scale, scale);
+    if constexpr (DITHER && LAT == HQ_E8) {
+        float d[8];   // in units of 2^-22
+        e8_dither(t.e0, d);
+        const float sd = __fmul_rn(scale, -0x1p-22f);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float2 x = f2_fma(make_float2(d[2 * j], d[2 * j + 1]), make_float2(sd, sd),
+                                    f2_mul(make_float2(u[2 * j], u[2 * j + 1]), s2));
+            w[j] = h2_pack(x.x, x.y);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float2 x = f2_mul(make_float2(u[2 * j], u[2 * j + 1]), s2);
+            w[j] = h2_pack(x.x, x.y);
+        }
+    }
+    t.e0 += LAT == HQ_E8 ? 4ull * kSplitGolden : 8ull;
 }
+__device__ __forceinline__ bool close_quarter(const Quarter &t) { return t.ok && t.bp <= t.nu * 32u; }
 
 // ------------------------------------------------------------------ segment starts
 // Where each 32-symbol segment of a chunk starts: seg[s] = 32 i + n says that terminator 32 s - 1 is
@@ -452,12 +487,12 @@ __device__ __forceinline__ uint32_t segment_start(const uint32_t *un, const uint
 }
 
 // ------------------------------------------------------------------ shared memory
-// MB: blocks of 16 query rows; RW: decoder rounds (8 tokens) of a warp in a step.  Half of the CTA's
-// warps decode K, half V: RW chunks of 32 tokens each in a step.
-template <int MB, int RW>
+// RW: decoder rounds (8 tokens) of a warp in a step of 32 RW tokens.  Half of the CTA's warps decode K,
+// half V: a chunk each (RW = 4), or a round of one chunk (RW = 1).
+template <int RW>
 struct AttnSmem {
-    static constexpr int R = 16 * MB, NT = 32 * RW, SP = NT + 8;
-    uint4 qh[MB * 8 * 32], ql[MB * 8 * 32];     // query fragments (two fp16 parts)
+    static constexpr int R = 16, NT = 32 * RW, SP = NT + 8;
+    uint4 qh[8 * 32], ql[8 * 32];               // query fragments (two fp16 parts)
     uint32_t v[NT * 64];                        // V: [token][128] fp16, 16-byte pieces swizzled by the token
     uint32_t p[R * (NT / 2)];                   // weights: [row][token] fp16, pieces swizzled by the row
     float sc[R * SP];                           // scores (log2)
@@ -472,6 +507,7 @@ struct AttnSmem {
     uint64_t range[3];
     int64_t span[2];                            // first and last position of the CTA's queries
     float eref[kAttnWarps];
+    TopRow top[kTop];
 };
 
 // Unnormalised H_128 of a row held 4 coordinates to a lane (4 lane ..), the whole warp.
@@ -521,20 +557,23 @@ __device__ __forceinline__ void rotate_query(const AttnArgs &a, float (&u)[4], c
 }
 
 // ------------------------------------------------------------------ what both kernels share
-// Chunks of a head that some query may see: [0, range[0]) and [range[1], range[2]).
-__device__ __forceinline__ void visible_range(const AttnArgs &a, uint64_t *range) {
-    const int64_t pmin = a.mask ? a.len - 1 : a.len - a.n_q;   // of any query: a bound is enough here
-    const uint64_t all = chunks_before(a, a.len, true);
-    uint64_t ia = all, ib = all;
-    if (a.window > 0) {
-        ia = a.sinks > 0 ? chunks_before(a, a.sinks < a.len ? a.sinks : a.len, true) : 0;
-        const int64_t lo = pmin - a.window + 1;
-        ib = lo > 0 ? chunks_before(a, lo, false) : 0;
-        if (ib < ia) ib = ia;
+// Chunks of a head that some query may see: [0, range[0]) and [range[1], range[2]), one bound each by the
+// first threads of warps 0 to 2 (range[0] and range[1] still to be put in order: see_bounds).
+__device__ __forceinline__ void visible_range(const Table &tab, uint64_t *range) {
+    const AttnArgs &a = tab.a;
+    if (threadIdx.x == 0) range[2] = chunks_before(tab, a.len, true);
+    if (threadIdx.x == 32 && a.window > 0)
+        range[0] = a.sinks > 0 ? chunks_before(tab, a.sinks < a.len ? a.sinks : a.len, true) : 0;
+    if (threadIdx.x == 64 && a.window > 0) {
+        const int64_t lo = (a.mask ? a.len - 1 : a.len - a.n_q) - a.window + 1;   // of any query: a bound is enough
+        range[1] = lo > 0 ? chunks_before(tab, lo, false) : 0;
     }
-    range[0] = ia;
-    range[1] = ib;
-    range[2] = all;
+}
+__device__ __forceinline__ void see_bounds(const AttnArgs &a, const uint64_t *range, uint64_t &ia, uint64_t &ib, uint64_t &ie) {
+    ie = range[2];
+    ia = a.window > 0 ? range[0] : ie;
+    ib = a.window > 0 ? range[1] : ie;
+    if (ib < ia) ib = ia;
 }
 // Bounds of the positions of query rows [row0, row0 + n): in order without a tree, at most their count
 // apart with one.
@@ -577,16 +616,11 @@ __device__ __forceinline__ void load_query(const AttnArgs &a, int head, int row,
 }
 // The largest of V's scales among the appends of visible chunks [v0, v1), over a warp (each warp takes its
 // share of the appends; the caller joins them): V is summed in its units.
-__device__ __forceinline__ float reference_scale(const AttnArgs &a, uint64_t nvis, uint64_t ia, uint64_t ib, uint64_t v0,
-                                                 uint64_t v1) {
+__device__ __forceinline__ float reference_scale(const Table &tab, uint64_t ia, uint64_t ib, uint64_t v0, uint64_t v1) {
     float e = 0.0f;
     if (v0 >= v1) return e;
-    AttnRow lo, hi;
-    load_row(a, 0, lo);
-    hi = lo;
-    find_row(a, v0 < ia ? v0 : v0 - ia + ib, lo);
-    find_row(a, v1 - 1 < ia ? v1 - 1 : v1 - 1 - ia + ib, hi);
-    for (uint64_t i = lo.append + threadIdx.x; i <= hi.append; i += blockDim.x) e = fmaxf(e, a.table[1][i].scale_inv);
+    const uint64_t lo = tab.append_of(v0 < ia ? v0 : v0 - ia + ib), hi = tab.append_of(v1 - 1 < ia ? v1 - 1 : v1 - 1 - ia + ib);
+    for (uint64_t i = lo + threadIdx.x; i <= hi; i += blockDim.x) e = fmaxf(e, tab.a.table[1][i].scale_inv);
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, m));
     return e;
@@ -607,11 +641,12 @@ struct Source {
         seed = a.seed[w];
         k = a.k[w];
         kl = a.k_last[w];
-        load_row(a, 0, row);
+        row.base = row.count = 0;   // none yet
     }
     // visible chunk v
-    __device__ __forceinline__ Piece piece(const AttnArgs &a, int head, uint64_t v, bool on, uint64_t nvis, uint64_t ia,
+    __device__ __forceinline__ Piece piece(const Table &tab, int head, uint64_t v, bool on, uint64_t nvis, uint64_t ia,
                                            uint64_t ib) {
+        const AttnArgs &a = tab.a;
         Piece p;
         p.on = on && v < nvis;
         p.ok = false;
@@ -621,7 +656,7 @@ struct Source {
         p.w0 = p.w1 = 0;
         if (p.on) {
             const uint64_t i = v < ia ? v : v - ia + ib;
-            find_row(a, i, row);
+            find_row(tab, i, row);
             const uint64_t j = i - row.base;
             p.t0 = row.row.token0 + 32 * (int64_t)j;
             const int64_t left = (int64_t)row.row.tokens - 32 * (int64_t)j;
@@ -680,37 +715,65 @@ __device__ __forceinline__ bool all_see(const AttnArgs &a, const Piece &p, const
     return p.on && p.n == 32 && tl < a.len && tl <= span[0] &&
            (a.window <= 0 || p.t0 > span[1] - a.window || tl < a.sinks);
 }
-// A tile that did not decode (one of its four lanes) or is not there counts as zeros, as a read stores it;
-// whether the warp saw one that did not.
-__device__ __forceinline__ bool zero_bad_tiles(bool valid, bool lane_ok, int lane, uint32_t (&w)[16]) {
-    const unsigned bad_lanes = __ballot_sync(0xffffffffu, valid && !lane_ok);
-    if (!valid || ((bad_lanes >> (lane & ~3)) & 0xFu)) {
-#pragma unroll
-        for (int j = 0; j < 16; j++) w[j] = 0u;
+// One round of a sound chunk: each lane decodes its quarter of a tile and hands every block (8 codes as 4
+// words) to `use`.  A lane whose tile is not there decodes the chunk's first segment and scales it to zero,
+// so the warp runs one path.  Returns the lanes whose tile did not decode.
+template <int LAT, bool DITHER, int FORM, bool STAGED, typename F>
+__device__ __forceinline__ unsigned decode_round(const uint32_t *p, const Planes &pl, const Source &src, const uint32_t *seg,
+                                                 uint32_t segi, bool valid, unsigned long long e0, float scale,
+                                                 const uint32_t *pairs, F &&use) {
+    if (!valid) {
+        segi &= 3u;
+        scale = 0.0f;
     }
-    return bad_lanes != 0u;
+    Quarter t;
+    open_quarter<LAT, FORM>(t, p, pl.nc, pl.nr, pl.nu, src.k, src.kl, src.seed,
+                           segment_start(p + pl.nc + pl.nr, seg, segi), segi, e0);
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+        uint32_t w[4];
+        decode_block<LAT, DITHER, FORM, STAGED>(t, src.k, src.kl, src.seed, scale, pairs, w);
+        use(g, w);
+    }
+    return __ballot_sync(0xffffffffu, valid && !close_quarter(t));
+}
+template <int LAT, bool DITHER, int FORM, typename F>
+__device__ __forceinline__ unsigned decode_round(bool ok, bool staged, const uint32_t *st, const uint32_t *gsrc,
+                                                 const Planes &pl, const Source &src, const uint32_t *seg, uint32_t segi,
+                                                 bool valid, unsigned long long e0, float scale, const uint32_t *pairs,
+                                                 F &&use) {
+    if (ok && staged) return decode_round<LAT, DITHER, FORM, true>(st, pl, src, seg, segi, valid, e0, scale, pairs, use);
+    if (ok) return decode_round<LAT, DITHER, FORM, false>(gsrc, pl, src, seg, segi, valid, e0, scale, pairs, use);
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+        const uint32_t w[4] = {0u, 0u, 0u, 0u};
+        use(g, w);
+    }
+    return 0u;
 }
 
-template <int LAT, bool DITHER, int FORM, int MB, int RW>
+template <int LAT, bool DITHER, int FORM, int RW>
 __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    using Smem = AttnSmem<MB, RW>;
+    using Smem = AttnSmem<RW>;
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     constexpr int R = Smem::R, NT = Smem::NT, SP = Smem::SP, KW = kAttnWarps / 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g8 = lane >> 2, t4 = lane & 3;
     const int split = blockIdx.x, head = blockIdx.y, row0 = blockIdx.z * R;
 
+    cudaTriggerProgrammaticLaunchCompletion();   // the combine may come up; it waits for this grid's end
     // ---- which chunks the queries can see, the queries themselves
-    if (threadIdx.x == 0) {
-        visible_range(a, sm.range);
-        query_span(a, row0, R, sm.span);
-    }
+    const Table tab(a, sm.top);
+    tab.load(sm.top);
+    if (threadIdx.x == 0) query_span(a, row0, R, sm.span);
     build_sign_table(sm.sign, 1, a.seed[0]);
     if (LAT == HQ_E8 && FORM == kFormUnary)
         for (int i = threadIdx.x; i < (1 << kPairBits); i += blockDim.x) sm.pairs[i] = pair_entry((uint32_t)i);
     for (int r = threadIdx.x; r < R; r += blockDim.x) sm.qpos[r] = query_position(a, row0 + r);
     __syncthreads();
+    visible_range(tab, sm.range);
+    __syncwarp();
     for (int r = warp; r < R; r += kAttnWarps) {
         float u[4], up;
         load_query(a, head, row0 + r, sm.sign, sm.xs[warp], lane, u, up);
@@ -722,14 +785,16 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
             const __half2 hh = *reinterpret_cast<const __half2 *>(&hi);
             const uint32_t lo = h2_pack(__fsub_rn(x0, __low2float(hh)), __fsub_rn(x1, __high2float(hh)));
             // coordinates 4 lane + 2 pr: quarter lane / 8, step lane % 8, register pair pr
-            const int slot = ((r >> 4) * 8 + (lane & 7)) * 32 + (r & 7) * 4 + (lane >> 3);
+            const int slot = (lane & 7) * 32 + (r & 7) * 4 + (lane >> 3);
             const int reg = ((r >> 3) & 1) + 2 * pr;
             reinterpret_cast<uint32_t *>(sm.qh)[slot * 4 + reg] = hi;
             reinterpret_cast<uint32_t *>(sm.ql)[slot * 4 + reg] = lo;
         }
         if (lane == 0) sm.qscale[r] = __fmul_rn(up, a.scale_log2);
     }
-    const uint64_t ia = sm.range[0], ib = sm.range[1], ie = sm.range[2];
+    __syncthreads();
+    uint64_t ia, ib, ie;
+    see_bounds(a, sm.range, ia, ib, ie);
     const uint64_t nvis = ia + (ie - ib);
     const uint64_t steps = (nvis + RW - 1) / RW;
     // this CTA's steps: an even share
@@ -737,21 +802,14 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
     const uint64_t st1 = steps * (uint64_t)(split + 1) / (uint64_t)a.splits;
 
     // ---- V is summed in units of the largest scale among this CTA's appends
-    float eref = reference_scale(a, nvis, ia, ib, st0 * RW, min(nvis, st1 * RW));
+    float eref = reference_scale(tab, ia, ib, st0 * RW, min(nvis, st1 * RW));
     if (lane == 0) sm.eref[warp] = eref;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kAttnWarps; i++) eref = fmaxf(eref, sm.eref[i]);
 
-    // softmax state of row tid / 16 (+ 16 mb), the same in its 16 threads but for the sums
-    float m_run[MB], l_run[MB], acc[2 * MB][4];
-#pragma unroll
-    for (int mb = 0; mb < MB; mb++) {
-        m_run[mb] = kNegInf;
-        l_run[mb] = 0.0f;
-    }
-#pragma unroll
-    for (int n = 0; n < 2 * MB; n++) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+    // softmax state of row tid / 16, the same in its 16 threads but for the sums
+    float m_run = kNegInf, l_run = 0.0f, acc[2][4] = {};
 
     // ---- this warp's part of a step: a chunk (RW = 4) or a round of one (RW = 1), of K or of V
     const int which = warp / KW, wi = warp % KW, ci = RW == 4 ? wi : 0;
@@ -759,13 +817,13 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
     src.init(a, which);
     uint32_t status = 0u;
     int buf = 0;
-    Piece cur = src.piece(a, head, st0 * RW + ci, st0 < st1, nvis, ia, ib);
+    Piece cur = src.piece(tab, head, st0 * RW + ci, st0 < st1, nvis, ia, ib);
     src.stage(cur, sm.stage[warp][0], lane, 32);
-    Piece next = src.piece(a, head, (st0 + 1) * RW + ci, st0 + 1 < st1, nvis, ia, ib);
+    Piece next = src.piece(tab, head, (st0 + 1) * RW + ci, st0 + 1 < st1, nvis, ia, ib);
     for (uint64_t step = st0; step < st1; step++, buf ^= 1) {
         // the next chunk's words behind this one's decode, and the offsets of the one after it
         src.stage(next, sm.stage[warp][buf ^ 1], lane, 32);
-        const Piece after = src.piece(a, head, (step + 2) * RW + ci, step + 2 < st1, nvis, ia, ib);
+        const Piece after = src.piece(tab, head, (step + 2) * RW + ci, step + 2 < st1, nvis, ia, ib);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
         Planes pl;
@@ -788,57 +846,55 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
         for (int rr = 0; rr < RW; rr++) {
             const int ti = 8 * (r0 + rr) + g8;
             const bool valid = cur.on && ti < cur.n;
-            uint32_t w[16];
-            bool lane_ok = ok;
-            if (ok && valid) {
-                const uint32_t segi = 32u * (uint32_t)(r0 + rr) + lane;
-                const unsigned long long e0 = (unsigned long long)(((cur.t0 + ti) * a.heads + head) * kTile);
-                if (staged)
-                    lane_ok = decode_quarter<LAT, DITHER, FORM, true>(st, pl.nc, pl.nr, pl.nu, src.k, src.kl,
-                                                                      segment_start(st + pl.nc + pl.nr, seg, segi), segi,
-                                                                      t4, e0, src.seed, zs, sm.pairs, w);
-                else
-                    lane_ok = decode_quarter<LAT, DITHER, FORM, false>(gsrc, pl.nc, pl.nr, pl.nu, src.k, src.kl,
-                                                                       segment_start(gsrc + pl.nc + pl.nr, seg, segi), segi,
-                                                                       t4, e0, src.seed, zs, sm.pairs, w);
-            }
-            bad |= zero_bad_tiles(valid, lane_ok, lane, w);
             const int tok = (RW == 4 ? 32 * wi + 8 * rr : 8 * wi);   // the round's first token in the step
+            uint32_t w[16];
+            const unsigned long long e0 = (unsigned long long)(((cur.t0 + ti) * a.heads + head) * kTile);
+            // a tile that did not decode counts as zeros, as a read stores it
+            const unsigned lost = decode_round<LAT, DITHER, FORM>(
+                ok, staged, st, gsrc, pl, src, seg, 32u * (uint32_t)(r0 + rr) + lane, valid, e0, zs, sm.pairs,
+                [&](int g, const uint32_t (&x)[4]) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) w[4 * g + i] = x[i];
+                });
+            float s[2][4] = {};
+            uint4 *const dst = reinterpret_cast<uint4 *>(sm.v + (tok + g8) * 64);
             if (which == 0) {
 #pragma unroll
-                for (int mb = 0; mb < MB; mb++) {
-                    float s[2][4] = {};
-#pragma unroll
-                    for (int st8 = 0; st8 < 8; st8++) {
-                        const uint4 fh = sm.qh[(mb * 8 + st8) * 32 + lane], fl = sm.ql[(mb * 8 + st8) * 32 + lane];
-                        const uint32_t ah[4] = {fh.x, fh.y, fh.z, fh.w}, al[4] = {fl.x, fl.y, fl.z, fl.w};
-                        mma16816(s[0], ah, w[2 * st8], w[2 * st8 + 1]);
-                        mma16816(s[1], al, w[2 * st8], w[2 * st8 + 1]);
-                    }
-#pragma unroll
-                    for (int hf = 0; hf < 2; hf++) {
-                        const int r = 16 * mb + 8 * hf + g8;
-                        const float qs = __fmul_rn(sm.qscale[r], ek);
-                        float x[2];
-#pragma unroll
-                        for (int cc = 0; cc < 2; cc++) {
-                            x[cc] = __fmul_rn(__fadd_rn(s[0][2 * hf + cc], s[1][2 * hf + cc]), qs);
-                            if (!open) {
-                                const int tc = 8 * (r0 + rr) + 2 * t4 + cc;
-                                const int64_t t = cur.t0 + tc, pos = sm.qpos[r];
-                                const bool see = cur.on && tc < cur.n && t < a.len && t <= pos &&
-                                                 (a.window <= 0 || t > pos - a.window || t < a.sinks);
-                                if (!see) x[cc] = kNegInf;
-                            }
-                        }
-                        *reinterpret_cast<float2 *>(sm.sc + r * SP + tok + 2 * t4) = make_float2(x[0], x[1]);
-                    }
+                for (int h = 0; h < 8; h++) {
+                    const uint4 fh = sm.qh[h * 32 + lane], fl = sm.ql[h * 32 + lane];
+                    const uint32_t ah[4] = {fh.x, fh.y, fh.z, fh.w}, al[4] = {fl.x, fl.y, fl.z, fl.w};
+                    mma16816(s[0], ah, w[2 * h], w[2 * h + 1]);
+                    mma16816(s[1], al, w[2 * h], w[2 * h + 1]);
                 }
             } else {
-                uint4 *dst = reinterpret_cast<uint4 *>(sm.v + (tok + g8) * 64);
 #pragma unroll
-                for (int c4 = 0; c4 < 4; c4++)
-                    dst[(4 * t4 + c4) ^ g8] = make_uint4(w[4 * c4], w[4 * c4 + 1], w[4 * c4 + 2], w[4 * c4 + 3]);
+                for (int g = 0; g < 4; g++)
+                    dst[(4 * t4 + g) ^ g8] = make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
+            }
+            bad |= lost != 0u;
+            if (which == 0) {
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++) {
+                    const int r = 8 * hf + g8;
+                    const float qs = __fmul_rn(sm.qscale[r], ek);
+                    float x[2];
+#pragma unroll
+                    for (int cc = 0; cc < 2; cc++) {
+                        x[cc] = __fmul_rn(__fadd_rn(s[0][2 * hf + cc], s[1][2 * hf + cc]), qs);
+                        if (lost && ((lost >> (4 * (2 * t4 + cc))) & 0xFu)) x[cc] = 0.0f;
+                        if (!open) {
+                            const int tc = 8 * (r0 + rr) + 2 * t4 + cc;
+                            const int64_t tt = cur.t0 + tc, pos = sm.qpos[r];
+                            const bool see = cur.on && tc < cur.n && tt < a.len && tt <= pos &&
+                                             (a.window <= 0 || tt > pos - a.window || tt < a.sinks);
+                            if (!see) x[cc] = kNegInf;
+                        }
+                    }
+                    *reinterpret_cast<float2 *>(sm.sc + r * SP + tok + 2 * t4) = make_float2(x[0], x[1]);
+                }
+            } else if ((lost >> (lane & ~3)) & 0xFu) {
+#pragma unroll
+                for (int g = 0; g < 4; g++) dst[(4 * t4 + g) ^ g8] = make_uint4(0u, 0u, 0u, 0u);
             }
         }
         if (bad) status |= HQ_ST_CORRUPT;
@@ -846,47 +902,44 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
         {
             // softmax: 16 threads to a row, NT / 16 tokens each
             constexpr int PT = NT / 16;
-#pragma unroll
-            for (int mb = 0; mb < MB; mb++) {
-                const int r = 16 * mb + (threadIdx.x >> 4), j = threadIdx.x & 15;
-                float x[PT];
-                const float *sc = sm.sc + r * SP + PT * j;
-                if constexpr (PT == 8) {
-                    const float4 y0 = reinterpret_cast<const float4 *>(sc)[0], y1 = reinterpret_cast<const float4 *>(sc)[1];
-                    x[0] = y0.x; x[1] = y0.y; x[2] = y0.z; x[3] = y0.w;
-                    x[4] = y1.x; x[5] = y1.y; x[6] = y1.z; x[7] = y1.w;
-                } else {
-                    const float2 y = *reinterpret_cast<const float2 *>(sc);
-                    x[0] = y.x; x[1] = y.y;
-                }
-                float m = m_run[mb];
-#pragma unroll
-                for (int i = 0; i < PT; i++) m = fmaxf(m, x[i]);
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const float base = m == kNegInf ? 0.0f : m;   // a row that has seen nothing yet: weights exp2(-inf) = 0
-                const float f = ex2(__fsub_rn(m_run[mb], base));
-                m_run[mb] = m;
-                if (j == 0) sm.rescale[r] = f;
-                float sum = 0.0f;
-#pragma unroll
-                for (int i = 0; i < PT; i++) {
-                    x[i] = ex2(__fsub_rn(x[i], base));
-                    sum = __fadd_rn(sum, x[i]);
-                }
-                l_run[mb] = __fmaf_rn(l_run[mb], f, sum);
-                if constexpr (PT == 8)
-                    *reinterpret_cast<uint4 *>(sm.p + r * (NT / 2) + 4 * (j ^ (r & 7))) =
-                        make_uint4(h2_pack(x[0], x[1]), h2_pack(x[2], x[3]), h2_pack(x[4], x[5]), h2_pack(x[6], x[7]));
-                else   // four pieces to a row of 32 tokens
-                    sm.p[r * (NT / 2) + 4 * ((j >> 2) ^ ((r >> 1) & 3)) + (j & 3)] = h2_pack(x[0], x[1]);
+            const int r = threadIdx.x >> 4, j = threadIdx.x & 15;
+            float x[PT];
+            const float *sc = sm.sc + r * SP + PT * j;
+            if constexpr (PT == 8) {
+                const float4 y0 = reinterpret_cast<const float4 *>(sc)[0], y1 = reinterpret_cast<const float4 *>(sc)[1];
+                x[0] = y0.x; x[1] = y0.y; x[2] = y0.z; x[3] = y0.w;
+                x[4] = y1.x; x[5] = y1.y; x[6] = y1.z; x[7] = y1.w;
+            } else {
+                const float2 y = *reinterpret_cast<const float2 *>(sc);
+                x[0] = y.x; x[1] = y.y;
             }
+            float m = m_run;
+#pragma unroll
+            for (int i = 0; i < PT; i++) m = fmaxf(m, x[i]);
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float base = m == kNegInf ? 0.0f : m;   // a row that has seen nothing yet: weights exp2(-inf) = 0
+            const float f = ex2(__fsub_rn(m_run, base));
+            m_run = m;
+            if (j == 0) sm.rescale[r] = f;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < PT; i++) {
+                x[i] = ex2(__fsub_rn(x[i], base));
+                sum = __fadd_rn(sum, x[i]);
+            }
+            l_run = __fmaf_rn(l_run, f, sum);
+            if constexpr (PT == 8)
+                *reinterpret_cast<uint4 *>(sm.p + r * (NT / 2) + 4 * (j ^ (r & 7))) =
+                    make_uint4(h2_pack(x[0], x[1]), h2_pack(x[2], x[3]), h2_pack(x[4], x[5]), h2_pack(x[6], x[7]));
+            else   // four pieces to a row of 32 tokens
+                sm.p[r * (NT / 2) + 4 * ((j >> 2) ^ ((r >> 1) & 3)) + (j & 3)] = h2_pack(x[0], x[1]);
         }
         __syncthreads();   // the weights are there
         {
             // sums of this warp's 16 coordinates over the step's tokens: V^T (16 x 16) times P^T (16 x 8 rows)
 #pragma unroll
-            for (int n = 0; n < 2 * MB; n++) {
+            for (int n = 0; n < 2; n++) {
                 const float f0 = sm.rescale[8 * n + 2 * t4], f1 = sm.rescale[8 * n + 2 * t4 + 1];
                 acc[n][0] = __fmul_rn(acc[n][0], f0);
                 acc[n][1] = __fmul_rn(acc[n][1], f1);
@@ -898,14 +951,11 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
                 uint32_t av[4];
                 const int tok = 16 * ks + 8 * (lane >> 4) + (lane & 7);
                 ldsm4t(av, sm.v + tok * 64 + 4 * ((2 * warp + ((lane >> 3) & 1)) ^ (tok & 7)));
-#pragma unroll
-                for (int n2 = 0; n2 < MB; n2++) {
-                    uint32_t bp[4];
-                    const int r = 16 * n2 + 8 * (lane >> 4) + (lane & 7), piece = 2 * ks + ((lane >> 3) & 1);
-                    ldsm4(bp, sm.p + r * (NT / 2) + 4 * (RW == 4 ? piece ^ (r & 7) : piece ^ ((r >> 1) & 3)));
-                    mma16816(acc[2 * n2], av, bp[0], bp[1]);
-                    mma16816(acc[2 * n2 + 1], av, bp[2], bp[3]);
-                }
+                uint32_t bp[4];
+                const int r = 8 * (lane >> 4) + (lane & 7), piece = 2 * ks + ((lane >> 3) & 1);
+                ldsm4(bp, sm.p + r * (NT / 2) + 4 * (RW == 4 ? piece ^ (r & 7) : piece ^ ((r >> 1) & 3)));
+                mma16816(acc[0], av, bp[0], bp[1]);
+                mma16816(acc[1], av, bp[2], bp[3]);
             }
         }
         __syncthreads();   // V, the scores and the weights may be written again
@@ -918,19 +968,18 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
     const int64_t pbase = ((int64_t)split * a.heads + head) * a.row_pad + row0;
     const float eo = __fmul_rn(eref, 64.0f);
 #pragma unroll
-    for (int n = 0; n < 2 * MB; n++) {
+    for (int n = 0; n < 2; n++) {
         float *o = a.part + (pbase + 8 * n + 2 * t4) * kTile + 16 * warp + g8;
         o[0] = __fmul_rn(acc[n][0], eo);
         o[kTile] = __fmul_rn(acc[n][1], eo);
         o[8] = __fmul_rn(acc[n][2], eo);
         o[kTile + 8] = __fmul_rn(acc[n][3], eo);
     }
-#pragma unroll
-    for (int mb = 0; mb < MB; mb++) {
-        float l = l_run[mb];
+    {
+        float l = l_run;
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, o));
-        if ((threadIdx.x & 15) == 0) a.ml[pbase + 16 * mb + (threadIdx.x >> 4)] = make_float2(m_run[mb], l);
+        if ((threadIdx.x & 15) == 0) a.ml[pbase + (threadIdx.x >> 4)] = make_float2(m_run, l);
     }
     status = __reduce_or_sync(0xffffffffu, status);
     if (lane == 0 && status) atomicOr(&a.stats[which]->status, status);
@@ -976,6 +1025,7 @@ struct WideSmem {
     float eref[16];
     uint32_t sign[4];
     uint32_t tmem;
+    TopRow top[kTop];
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -1045,9 +1095,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
     const int g8 = lane >> 2, t4 = lane & 3;
     const int split = blockIdx.x, head = blockIdx.y, row0 = blockIdx.z * kWideRows;
     const int rows = min(a.rows - row0, kWideRows), nb = rows > 128 ? 2 : 1;
+    cudaTriggerProgrammaticLaunchCompletion();   // the combine may come up; it waits for this grid's end
 
     if (threadIdx.x == 0) {
-        visible_range(a, sm.range);
         query_span(a, row0, rows, sm.span);
         for (int i = 0; i < 2; i++)
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&sm.bar[i])) : "memory");
@@ -1057,6 +1107,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    const Table tab(a, sm.top);
+    tab.load(sm.top);
     build_sign_table(sm.sign, 1, a.seed[0]);
     if (LAT == HQ_E8 && FORM == kFormUnary)
         for (int i = threadIdx.x; i < (1 << kPairBits); i += blockDim.x) sm.pairs[i] = pair_entry((uint32_t)i);
@@ -1066,6 +1118,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tm = sm.tmem, tmS = tm + 256u, tmQ = tm + 384u;
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;   // this warp's 32 TMEM lanes (lane in bits 16..)
+    visible_range(tab, sm.range);
+    __syncwarp();
 
     // ---- queries: upper parts to their tiles, lower parts through the K and V tiles to TMEM
     for (int r = warp; r < 128 * nb; r += 16) {
@@ -1094,11 +1148,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
         }
         tmem_st16(tmQ + 64u * b + 16u * grp + lane_base, r);
     }
-    const uint64_t ia = sm.range[0], ib = sm.range[1], ie = sm.range[2];
+    uint64_t ia, ib, ie;
+    see_bounds(a, sm.range, ia, ib, ie);
     const uint64_t nvis = ia + (ie - ib), steps = (nvis + 3) / 4;
     const uint64_t st0 = steps * (uint64_t)split / (uint64_t)a.splits;
     const uint64_t st1 = steps * (uint64_t)(split + 1) / (uint64_t)a.splits;
-    float eref = reference_scale(a, nvis, ia, ib, st0 * 4, min(nvis, st1 * 4));
+    float eref = reference_scale(tab, ia, ib, st0 * 4, min(nvis, st1 * 4));
     if (lane == 0) sm.eref[warp] = eref;
     __syncthreads();
 #pragma unroll
@@ -1112,12 +1167,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
     bool dead = false;
     int buf = 0;
     uint32_t s_count = 0;   // commits of S so far
-    Piece cur = src.piece(a, head, st0 * 4 + ci, st0 < st1, nvis, ia, ib);
+    Piece cur = src.piece(tab, head, st0 * 4 + ci, st0 < st1, nvis, ia, ib);
     src.stage(cur, sm.stage[chunk_slot][0], threadIdx.x & 63, 64);
-    Piece next = src.piece(a, head, (st0 + 1) * 4 + ci, st0 + 1 < st1, nvis, ia, ib);
+    Piece next = src.piece(tab, head, (st0 + 1) * 4 + ci, st0 + 1 < st1, nvis, ia, ib);
     for (uint64_t step = st0; step < st1; step++, buf ^= 1) {
         src.stage(next, sm.stage[chunk_slot][buf ^ 1], threadIdx.x & 63, 64);
-        const Piece after = src.piece(a, head, (step + 2) * 4 + ci, step + 2 < st1, nvis, ia, ib);
+        const Piece after = src.piece(tab, head, (step + 2) * 4 + ci, step + 2 < st1, nvis, ia, ib);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         // the chunk's words come from both of its warps
         asm volatile("bar.sync %0, 64;" ::"r"(1 + chunk_slot) : "memory");
@@ -1147,27 +1202,21 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
         for (int rr = 0; rr < 2; rr++) {
             const int ti = 8 * (r0 + rr) + g8;
             const bool valid = cur.on && ti < cur.n;
-            uint32_t w[16];
-            bool lane_ok = ok;
-            if (ok && valid) {
-                const uint32_t segi = 32u * (uint32_t)(r0 + rr) + lane;
-                const unsigned long long e0 = (unsigned long long)(((cur.t0 + ti) * a.heads + head) * kTile);
-                if (staged)
-                    lane_ok = decode_quarter<LAT, DITHER, FORM, true>(st, pl.nc, pl.nr, pl.nu, src.k, src.kl,
-                                                                      segment_start(st + pl.nc + pl.nr, seg, segi), segi,
-                                                                      t4, e0, src.seed, zs, sm.pairs, w);
-                else
-                    lane_ok = decode_quarter<LAT, DITHER, FORM, false>(gsrc, pl.nc, pl.nr, pl.nu, src.k, src.kl,
-                                                                       segment_start(gsrc + pl.nc + pl.nr, seg, segi), segi,
-                                                                       t4, e0, src.seed, zs, sm.pairs, w);
-            }
-            bad |= zero_bad_tiles(valid, lane_ok, lane, w);
             // token 32 ci + ti: panel t4 / 2, pieces 4 (t4 & 1) ..
-            const int t = 32 * ci + ti;
+            const int tok = 32 * ci + ti;
+            uint4 *const dst = tile + (t4 >> 1) * 1024 + tok * 8;
+            const unsigned long long e0 = (unsigned long long)(((cur.t0 + ti) * a.heads + head) * kTile);
+            // a tile that did not decode counts as zeros, as a read stores it
+            const unsigned lost = decode_round<LAT, DITHER, FORM>(
+                ok, staged, st, gsrc, pl, src, seg, 32u * (uint32_t)(r0 + rr) + lane, valid, e0, zs, sm.pairs,
+                [&](int g, const uint32_t (&w)[4]) {
+                    dst[(4 * (t4 & 1) + g) ^ (tok & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
+                });
+            bad |= lost != 0u;
+            if ((lost >> (lane & ~3)) & 0xFu) {
 #pragma unroll
-            for (int c4 = 0; c4 < 4; c4++)
-                tile[(t4 >> 1) * 1024 + t * 8 + ((4 * (t4 & 1) + c4) ^ (t & 7))] =
-                    make_uint4(w[4 * c4], w[4 * c4 + 1], w[4 * c4 + 2], w[4 * c4 + 3]);
+                for (int g = 0; g < 4; g++) dst[(4 * (t4 & 1) + g) ^ (tok & 7)] = make_uint4(0u, 0u, 0u, 0u);
+            }
         }
         if (bad) status |= HQ_ST_CORRUPT;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1309,15 +1358,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
     if (lane == 0 && status) atomicOr(&a.stats[which]->status, status);
 }
 
-template <int LAT, bool DITHER, int FORM, int MB, int RW>
+template <int LAT, bool DITHER, int FORM, int RW>
 cudaError_t launch_rw(const AttnArgs &a, cudaStream_t s) {
-    auto kern = attention_kernel<LAT, DITHER, FORM, MB, RW>;
+    auto kern = attention_kernel<LAT, DITHER, FORM, RW>;
     static LaunchPlan plan;
-    const size_t smem = sizeof(AttnSmem<MB, RW>);
+    const size_t smem = sizeof(AttnSmem<RW>);
     unsigned grid = 0;
     cudaError_t e = plan.grid(kern, kAttnWarps * 32, smem, 1, grid);
     if (e != cudaSuccess) return e;
-    const dim3 g((unsigned)a.splits, (unsigned)a.heads, (unsigned)(a.row_pad / (16 * MB)));
+    const dim3 g((unsigned)a.splits, (unsigned)a.heads, (unsigned)(a.row_pad / 16));
     kern<<<g, kAttnWarps * 32, smem, s>>>(a);
     return cudaGetLastError();
 }
@@ -1338,15 +1387,13 @@ cudaError_t launch_wide(const AttnArgs &a, cudaStream_t s) {
 template <int LAT, bool DITHER, int FORM>
 cudaError_t launch_form(const AttnArgs &a, cudaStream_t s) {
     if (a.rows > kNarrowRows) return launch_wide<LAT, DITHER, FORM>(a, s);
-    return a.short_steps ? launch_rw<LAT, DITHER, FORM, 1, 1>(a, s) : launch_rw<LAT, DITHER, FORM, 1, 4>(a, s);
+    return a.short_steps ? launch_rw<LAT, DITHER, FORM, 1>(a, s) : launch_rw<LAT, DITHER, FORM, 4>(a, s);
 }
 
 template <int LAT, bool DITHER>
 cudaError_t launch_lat(const AttnArgs &a, cudaStream_t s) {
     if (a.k[0] == 0 && a.k[1] == 0 && a.k_last[0] == 0 && a.k_last[1] == 0) return launch_form<LAT, DITHER, kFormUnary>(a, s);
-    if (a.k[0] > 4 || a.k[1] > 4 || a.k_last[0] != a.k[0] || a.k_last[1] != a.k[1])
-        return launch_form<LAT, DITHER, kFormGeneral>(a, s);
-    return launch_form<LAT, DITHER, kFormWindows>(a, s);
+    return launch_form<LAT, DITHER, kFormGeneral>(a, s);
 }
 
 }  // namespace
