@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libhq.so")
 SOURCES = ["hq_api.cu", "hq_encode.cu", "hq_decode.cu", "hq_consume.cu", "hq_static.cu", "hq_debug.cu",
            "hq_rot_encode.cu", "hq_rot_decode.cu", "hq_haar.cu", "hq_shard.cu", "hq_rope.cu", "hq_repack.cu",
            "hq_attention.cu", "hq_attention_z.cu", "hq_attention_a2.cu", "hq_attention_d4.cu", "hq_attention_e8.cu"]
-HEADERS = ["hq_internal.h", "hq_device.cuh", "hq_encode.cuh", "hq_decode.cuh", "hq_attention.cuh"]
+HEADERS = ["hq_internal.h", "hq_device.cuh", "hq_encode.cuh", "hq_decode.cuh", "hq_table.cuh", "hq_attention.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 NVCC_FLAGS = [
@@ -38,9 +38,11 @@ NVCC_FLAGS = [
 def _stale(obj: str, src: str) -> bool:
     if not os.path.exists(obj):
         return True
-    own = os.path.basename(src).startswith("hq_attention")   # the only sources that include hq_attention.cuh
-    deps = [src, os.path.join(INCLUDE, "hq.h")] + [os.path.join(CSRC, h) for h in HEADERS
-                                                   if own or h != "hq_attention.cuh"]
+    name = os.path.basename(src)
+    skip = set()   # headers that few sources include
+    if not name.startswith("hq_attention"):
+        skip = {"hq_attention.cuh"} if name == "hq_repack.cu" else {"hq_attention.cuh", "hq_table.cuh"}
+    deps = [src, os.path.join(INCLUDE, "hq.h")] + [os.path.join(CSRC, h) for h in HEADERS if h not in skip]
     t = os.path.getmtime(obj)
     return any(os.path.getmtime(d) > t for d in deps)
 

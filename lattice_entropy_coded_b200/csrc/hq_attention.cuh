@@ -29,6 +29,7 @@
 #include <stdint.h>
 
 #include "hq_decode.cuh"
+#include "hq_table.cuh"
 
 namespace hq {
 
@@ -135,55 +136,14 @@ __device__ __forceinline__ void load_row(const AttnArgs &a, uint64_t append, Att
     r.base = base;
     r.count = (uint64_t)(((int64_t)r.row.tokens + 31) / 32);
 }
-// The append table is searched through a sample of it in shared memory (all of it up to kTop appends):
-// one load's latency for the sample instead of one for every step of a search, which on a short cache
-// was most of the kernel's time.
-constexpr int kTop = 128;
-struct TopRow {
-    uint64_t first_chunk;
-    int64_t token0;
-};
-struct Table {
-    const AttnArgs &a;
-    const TopRow *top;
-    uint64_t stride, n;   // sample s is append s * stride
-    __device__ __forceinline__ Table(const AttnArgs &args, TopRow *t) : a(args), top(t) {
-        stride = (a.n_appends + kTop - 1) / kTop;
-        n = (a.n_appends + stride - 1) / stride;
-    }
-    // by the whole CTA; the caller synchronises
-    __device__ __forceinline__ void load(TopRow *t) const {
-        for (uint64_t i = threadIdx.x; i < n; i += blockDim.x)
-            t[i] = *reinterpret_cast<const TopRow *>(&a.table[0][i * stride]);
-    }
-    // the last append whose first chunk is at most x (by chunk), or whose first token is (else); 0 if none
-    template <bool CHUNK>
-    __device__ __forceinline__ uint64_t find(int64_t x) const {
-        uint64_t lo = 0, hi = n - 1;
-        while (lo < hi) {
-            const uint64_t mid = (lo + hi + 1) >> 1;
-            if ((CHUNK ? (int64_t)top[mid].first_chunk : top[mid].token0) <= x) lo = mid; else hi = mid - 1;
-        }
-        if (stride == 1) return lo;
-        lo *= stride;
-        hi = min(lo + stride, a.n_appends) - 1;
-        while (lo < hi) {
-            const uint64_t mid = (lo + hi + 1) >> 1;
-            if ((CHUNK ? (int64_t)a.table[0][mid].first_chunk : a.table[0][mid].token0) <= x) lo = mid; else hi = mid - 1;
-        }
-        return lo;
-    }
-    // the append of per-head chunk i
-    __device__ __forceinline__ uint64_t append_of(uint64_t i) const { return find<true>((int64_t)(i * (uint64_t)a.heads)); }
-};
-__device__ __forceinline__ void find_row(const Table &t, uint64_t i, AttnRow &r) {
+__device__ __forceinline__ void find_row(const AttnArgs &a, const Table &t, uint64_t i, AttnRow &r) {
     if (i >= r.base && i < r.base + r.count) return;
-    load_row(t.a, t.append_of(i), r);
+    load_row(a, t.append_of(i), r);
 }
 // Per-head chunks that lie wholly before token t (round_up: that hold any token before t).
-__device__ __forceinline__ uint64_t chunks_before(const Table &tab, int64_t t, bool round_up) {
+__device__ __forceinline__ uint64_t chunks_before(const AttnArgs &a, const Table &tab, int64_t t, bool round_up) {
     AttnRow r;
-    load_row(tab.a, tab.find<false>(t), r);
+    load_row(a, tab.append_of_token(t), r);
     const int64_t in = t - r.row.token0;
     if (in <= 0) return r.base;
     const uint64_t n = (uint64_t)(round_up ? (in + 31) / 32 : in / 32);
@@ -559,14 +519,13 @@ __device__ __forceinline__ void rotate_query(const AttnArgs &a, float (&u)[4], c
 // ------------------------------------------------------------------ what both kernels share
 // Chunks of a head that some query may see: [0, range[0]) and [range[1], range[2]), one bound each by the
 // first threads of warps 0 to 2 (range[0] and range[1] still to be put in order: see_bounds).
-__device__ __forceinline__ void visible_range(const Table &tab, uint64_t *range) {
-    const AttnArgs &a = tab.a;
-    if (threadIdx.x == 0) range[2] = chunks_before(tab, a.len, true);
+__device__ __forceinline__ void visible_range(const AttnArgs &a, const Table &tab, uint64_t *range) {
+    if (threadIdx.x == 0) range[2] = chunks_before(a, tab, a.len, true);
     if (threadIdx.x == 32 && a.window > 0)
-        range[0] = a.sinks > 0 ? chunks_before(tab, a.sinks < a.len ? a.sinks : a.len, true) : 0;
+        range[0] = a.sinks > 0 ? chunks_before(a, tab, a.sinks < a.len ? a.sinks : a.len, true) : 0;
     if (threadIdx.x == 64 && a.window > 0) {
         const int64_t lo = (a.mask ? a.len - 1 : a.len - a.n_q) - a.window + 1;   // of any query: a bound is enough
-        range[1] = lo > 0 ? chunks_before(tab, lo, false) : 0;
+        range[1] = lo > 0 ? chunks_before(a, tab, lo, false) : 0;
     }
 }
 __device__ __forceinline__ void see_bounds(const AttnArgs &a, const uint64_t *range, uint64_t &ia, uint64_t &ib, uint64_t &ie) {
@@ -616,11 +575,11 @@ __device__ __forceinline__ void load_query(const AttnArgs &a, int head, int row,
 }
 // The largest of V's scales among the appends of visible chunks [v0, v1), over a warp (each warp takes its
 // share of the appends; the caller joins them): V is summed in its units.
-__device__ __forceinline__ float reference_scale(const Table &tab, uint64_t ia, uint64_t ib, uint64_t v0, uint64_t v1) {
+__device__ __forceinline__ float reference_scale(const AttnArgs &a, const Table &tab, uint64_t ia, uint64_t ib, uint64_t v0, uint64_t v1) {
     float e = 0.0f;
     if (v0 >= v1) return e;
     const uint64_t lo = tab.append_of(v0 < ia ? v0 : v0 - ia + ib), hi = tab.append_of(v1 - 1 < ia ? v1 - 1 : v1 - 1 - ia + ib);
-    for (uint64_t i = lo + threadIdx.x; i <= hi; i += blockDim.x) e = fmaxf(e, tab.a.table[1][i].scale_inv);
+    for (uint64_t i = lo + threadIdx.x; i <= hi; i += blockDim.x) e = fmaxf(e, a.table[1][i].scale_inv);
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, m));
     return e;
@@ -644,9 +603,8 @@ struct Source {
         row.base = row.count = 0;   // none yet
     }
     // visible chunk v
-    __device__ __forceinline__ Piece piece(const Table &tab, int head, uint64_t v, bool on, uint64_t nvis, uint64_t ia,
+    __device__ __forceinline__ Piece piece(const AttnArgs &a, const Table &tab, int head, uint64_t v, bool on, uint64_t nvis, uint64_t ia,
                                            uint64_t ib) {
-        const AttnArgs &a = tab.a;
         Piece p;
         p.on = on && v < nvis;
         p.ok = false;
@@ -656,7 +614,7 @@ struct Source {
         p.w0 = p.w1 = 0;
         if (p.on) {
             const uint64_t i = v < ia ? v : v - ia + ib;
-            find_row(tab, i, row);
+            find_row(a, tab, i, row);
             const uint64_t j = i - row.base;
             p.t0 = row.row.token0 + 32 * (int64_t)j;
             const int64_t left = (int64_t)row.row.tokens - 32 * (int64_t)j;
@@ -764,7 +722,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
 
     cudaTriggerProgrammaticLaunchCompletion();   // the combine may come up; it waits for this grid's end
     // ---- which chunks the queries can see, the queries themselves
-    const Table tab(a, sm.top);
+    const Table tab(a.table[0], a.n_appends, a.heads, sm.top);
     tab.load(sm.top);
     if (threadIdx.x == 0) query_span(a, row0, R, sm.span);
     build_sign_table(sm.sign, 1, a.seed[0]);
@@ -772,7 +730,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
         for (int i = threadIdx.x; i < (1 << kPairBits); i += blockDim.x) sm.pairs[i] = pair_entry((uint32_t)i);
     for (int r = threadIdx.x; r < R; r += blockDim.x) sm.qpos[r] = query_position(a, row0 + r);
     __syncthreads();
-    visible_range(tab, sm.range);
+    visible_range(a, tab, sm.range);
     __syncwarp();
     for (int r = warp; r < R; r += kAttnWarps) {
         float u[4], up;
@@ -802,7 +760,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
     const uint64_t st1 = steps * (uint64_t)(split + 1) / (uint64_t)a.splits;
 
     // ---- V is summed in units of the largest scale among this CTA's appends
-    float eref = reference_scale(tab, ia, ib, st0 * RW, min(nvis, st1 * RW));
+    float eref = reference_scale(a, tab, ia, ib, st0 * RW, min(nvis, st1 * RW));
     if (lane == 0) sm.eref[warp] = eref;
     __syncthreads();
 #pragma unroll
@@ -817,13 +775,13 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
     src.init(a, which);
     uint32_t status = 0u;
     int buf = 0;
-    Piece cur = src.piece(tab, head, st0 * RW + ci, st0 < st1, nvis, ia, ib);
+    Piece cur = src.piece(a, tab, head, st0 * RW + ci, st0 < st1, nvis, ia, ib);
     src.stage(cur, sm.stage[warp][0], lane, 32);
-    Piece next = src.piece(tab, head, (st0 + 1) * RW + ci, st0 + 1 < st1, nvis, ia, ib);
+    Piece next = src.piece(a, tab, head, (st0 + 1) * RW + ci, st0 + 1 < st1, nvis, ia, ib);
     for (uint64_t step = st0; step < st1; step++, buf ^= 1) {
         // the next chunk's words behind this one's decode, and the offsets of the one after it
         src.stage(next, sm.stage[warp][buf ^ 1], lane, 32);
-        const Piece after = src.piece(tab, head, (step + 2) * RW + ci, step + 2 < st1, nvis, ia, ib);
+        const Piece after = src.piece(a, tab, head, (step + 2) * RW + ci, step + 2 < st1, nvis, ia, ib);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
         Planes pl;
@@ -1107,7 +1065,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    const Table tab(a, sm.top);
+    const Table tab(a.table[0], a.n_appends, a.heads, sm.top);
     tab.load(sm.top);
     build_sign_table(sm.sign, 1, a.seed[0]);
     if (LAT == HQ_E8 && FORM == kFormUnary)
@@ -1118,7 +1076,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tm = sm.tmem, tmS = tm + 256u, tmQ = tm + 384u;
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;   // this warp's 32 TMEM lanes (lane in bits 16..)
-    visible_range(tab, sm.range);
+    visible_range(a, tab, sm.range);
     __syncwarp();
 
     // ---- queries: upper parts to their tiles, lower parts through the K and V tiles to TMEM
@@ -1153,7 +1111,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
     const uint64_t nvis = ia + (ie - ib), steps = (nvis + 3) / 4;
     const uint64_t st0 = steps * (uint64_t)split / (uint64_t)a.splits;
     const uint64_t st1 = steps * (uint64_t)(split + 1) / (uint64_t)a.splits;
-    float eref = reference_scale(tab, ia, ib, st0 * 4, min(nvis, st1 * 4));
+    float eref = reference_scale(a, tab, ia, ib, st0 * 4, min(nvis, st1 * 4));
     if (lane == 0) sm.eref[warp] = eref;
     __syncthreads();
 #pragma unroll
@@ -1167,12 +1125,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
     bool dead = false;
     int buf = 0;
     uint32_t s_count = 0;   // commits of S so far
-    Piece cur = src.piece(tab, head, st0 * 4 + ci, st0 < st1, nvis, ia, ib);
+    Piece cur = src.piece(a, tab, head, st0 * 4 + ci, st0 < st1, nvis, ia, ib);
     src.stage(cur, sm.stage[chunk_slot][0], threadIdx.x & 63, 64);
-    Piece next = src.piece(tab, head, (st0 + 1) * 4 + ci, st0 + 1 < st1, nvis, ia, ib);
+    Piece next = src.piece(a, tab, head, (st0 + 1) * 4 + ci, st0 + 1 < st1, nvis, ia, ib);
     for (uint64_t step = st0; step < st1; step++, buf ^= 1) {
         src.stage(next, sm.stage[chunk_slot][buf ^ 1], threadIdx.x & 63, 64);
-        const Piece after = src.piece(tab, head, (step + 2) * 4 + ci, step + 2 < st1, nvis, ia, ib);
+        const Piece after = src.piece(a, tab, head, (step + 2) * 4 + ci, step + 2 < st1, nvis, ia, ib);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         // the chunk's words come from both of its warps
         asm volatile("bar.sync %0, 64;" ::"r"(1 + chunk_slot) : "memory");

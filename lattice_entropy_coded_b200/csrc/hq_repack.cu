@@ -3,26 +3,27 @@
 // starts (its dither counter is its position), so nothing is decoded: a tile's bits are one
 // run of each plane of its chunk, and a new chunk's planes are those runs joined.
 //
-// Two launches.  The first finds, one warp to a new chunk, each tile's chunk in the source
-// and the run of its unary bits there (the 128-th terminators, by population counts), and
-// writes 16 bytes per tile and the new chunk's words.  The second sums the words of the
-// chunks before its own (contiguous) chunks, which costs each CTA a few bytes per chunk
-// read from L2 and no third launch, and assembles the planes, a lane to a word: every word
-// joins the bits of at most two tiles (a tile holds 128 unary bits or more, 16 coset bits,
-// and at least 64 remainder bits where it has any).
-// Bound: the stream's bytes, read twice (the second time from L2 up to its size) and
-// written once.
+// Two launches.  The first finds, one warp to a new chunk, each tile's chunk in the source and the
+// run of its unary bits there, and writes 16 bytes per tile and the new chunk's words.  A new chunk
+// that is a whole chunk of the source (a fork of full chunks) needs only its terminators counted;
+// else the warp finds every 128th terminator of each chunk it touches, and tiles in chunks of their
+// own (one-token appends) are counted by their lanes.  The second launch sums the words before its
+// chunks and copies the planes run by run (tiles that follow one another in one source chunk), a lane
+// to a word: a funnel shift of two source words, and a second pair where two runs meet in a word
+// (never three: a tile has 128 unary bits or more, 16 coset bits, 64 remainder bits or none).
+// Bound: the stream's bytes, read twice (the second time from L2 up to its size) and written once.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "hq_device.cuh"
+#include "hq_decode.cuh"
+#include "hq_table.cuh"
 
 namespace hq {
 
 namespace {
 
 constexpr int kMaxRanges = 32;
-constexpr int kRepackWarps = 8;
+constexpr int kRepackWarps = 4;
 
 struct RepackRange {
     int64_t begin, end;
@@ -45,21 +46,12 @@ struct RepackArgs {
     hq_stats *stats;
     uint4 *tiles;          // per new tile: source chunk's first word | tile << 48 | its tiles << 56, unary start, length
     uint32_t *sizes;       // per new chunk: words
+    uint64_t *sums;        // per CTA of the first launch: words of its chunks
     uint64_t n_chunks;
     int heads, n_ranges, e8;
     uint32_t rem_bits;     // remainder bits of a tile
     RepackRange range[kMaxRanges];
 };
-
-// Append row of the last append that starts at or before token t (row 0 if none).
-__device__ __forceinline__ uint64_t row_of_token(const hq_kv_append_row *table, uint64_t n, int64_t t) {
-    uint64_t lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const uint64_t mid = (lo + hi + 1) >> 1;
-        if (table[mid].token0 <= t) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-}
 
 // 32 bits of the stream from absolute bit b on; `need` of them are used, and the second word is
 // read only if they reach into it.
@@ -97,48 +89,65 @@ __device__ __forceinline__ NewChunk new_chunk(const RepackArgs &a, uint64_t c) {
 }
 
 // First unary bit of every tile of a chunk of n tiles (start[0 .. n]) by the whole warp; false unless
-// the plane of nu words holds exactly 128 n terminators.
+// the plane of nu words holds exactly 128 n terminators.  64 words at a time, as the attention's scan:
+// population counts, two sets of 32 scanned in one register; a word that holds the last terminator of a
+// tile (at most one) notes itself, and each lane then finds its tile's bit.
 __device__ __forceinline__ bool tile_starts(const uint32_t *un, uint32_t nu, uint32_t n, uint32_t *start, int lane) {
     uint32_t seen = 0;
-    if (lane == 0) start[0] = 0;
+    __syncwarp();   // the last chunk's starts have been read
     for (uint32_t i0 = 0; i0 < nu; i0 += 128) {
-        uint32_t w[4];
+        uint32_t p[4];
 #pragma unroll
         for (int u = 0; u < 4; u++) {
             const uint32_t i = i0 + 32u * u + lane;
-            w[u] = i < nu ? __ldg(un + i) : 0u;
+            p[u] = i < nu ? __popc(__ldg(un + i)) : 0u;
         }
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-            const uint32_t p = __popc(w[u]);
-            uint32_t incl = p;
+        for (int h = 0; h < 2; h++) {
+            uint32_t both = p[2 * h] | p[2 * h + 1] << 16;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
+                const uint32_t v = __shfl_up_sync(0xffffffffu, both, o);
+                if (lane >= o) both += v;
             }
-            const uint32_t before = seen + incl - p;
-            // the word holds terminators before .. before + p - 1; number 128 t - 1 ends tile t - 1
-            const uint32_t t = (before + 128u) >> 7;
-            if (128u * t - 1u < before + p && t <= n) {
-                uint32_t x = w[u];
-                for (uint32_t d = 128u * t - 1u - before; d; d--) x &= x - 1u;
-                start[t] = (i0 + 32u * u + lane) * 32u + (uint32_t)__ffs((int)x);
-            }
-            seen += __shfl_sync(0xffffffffu, incl, 31);
+            const uint32_t all = __shfl_sync(0xffffffffu, both, 31);
+            const uint32_t b0 = seen + (both & 0xFFFFu) - p[2 * h];
+            const uint32_t b1 = seen + (all & 0xFFFFu) + (both >> 16) - p[2 * h + 1];
+            const uint32_t i = i0 + 64u * h + lane;
+            // word i holds terminators b .. b + p - 1; number 128 t - 1 ends tile t - 1
+            if ((b0 >> 7) != ((b0 + p[2 * h]) >> 7) && b0 < 128u * n) start[(b0 >> 7) + 1u] = i * 32u + (127u - (b0 & 127u));
+            if ((b1 >> 7) != ((b1 + p[2 * h + 1]) >> 7) && b1 < 128u * n)
+                start[(b1 >> 7) + 1u] = (i + 32u) * 32u + (127u - (b1 & 127u));
+            seen += (all & 0xFFFFu) + (all >> 16);
         }
     }
     __syncwarp();
-    return seen == 128u * n;
+    if (seen != 128u * n) return false;
+    uint32_t v = 0;
+    if ((uint32_t)lane < n) {
+        v = start[lane + 1];
+        v = (v & ~31u) + select_bit(__ldg(un + (v >> 5)), v & 31u) + 1u;
+    }
+    __syncwarp();
+    if ((uint32_t)lane < n) start[lane + 1] = v;
+    if (lane == 0) start[0] = 0;
+    __syncwarp();
+    return true;
 }
 
 __global__ void __launch_bounds__(kRepackWarps * 32) repack_measure(const __grid_constant__ RepackArgs a) {
     __shared__ uint32_t starts[kRepackWarps][36];
+    __shared__ TopRow top[kTop];
+    __shared__ uint32_t size_of[kRepackWarps];
+    cudaTriggerProgrammaticLaunchCompletion();   // the second launch may come up; it waits for this grid's end
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Table tab(a.src_table, a.src_appends, a.heads, top);
+    tab.load(top);
+    __syncthreads();
     if (blockIdx.x == 0) {
         if (threadIdx.x < (unsigned)a.n_ranges) {
             const RepackRange r = a.range[threadIdx.x];
-            hq_kv_append_row row = a.src_table[row_of_token(a.src_table, a.src_appends, r.begin)];
+            hq_kv_append_row row = a.src_table[tab.append_of_token(r.begin)];
             row.first_chunk = r.first_chunk;
             row.token0 = r.begin;
             row.tokens = (int32_t)(r.end - r.begin);
@@ -152,87 +161,116 @@ __global__ void __launch_bounds__(kRepackWarps * 32) repack_measure(const __grid
         }
     }
     const uint64_t c = (uint64_t)blockIdx.x * kRepackWarps + warp;
-    if (c >= a.n_chunks) return;
-    const NewChunk g = new_chunk(a, c);
-    // the lane's token in the source; its scale has to be that of the range's first token
-    const int64_t t = g.t0 + ((uint32_t)lane < g.n ? lane : (int)g.n - 1);
-    const hq_kv_append_row ref = a.src_table[row_of_token(a.src_table, a.src_appends, a.range[g.r].begin)];
-    const hq_kv_append_row row = a.src_table[row_of_token(a.src_table, a.src_appends, t)];
-    const int64_t in = t - row.token0;
-    bool ok = in >= 0 && in < row.tokens && __float_as_uint(row.alpha) == __float_as_uint(ref.alpha) &&
-              __float_as_uint(row.scale_inv) == __float_as_uint(ref.scale_inv);
-    uint64_t chunk = 0, w0 = 0;
-    uint32_t n = 0, nu = 0, head_words = 0;
-    const uint32_t ti = (uint32_t)in & 31u;
-    if (ok) {
-        const int64_t left = (int64_t)row.tokens - (in & ~INT64_C(31));
-        n = (uint32_t)(left < 32 ? left : 32);
-        chunk = row.first_chunk + (uint64_t)g.h * (uint64_t)(((int64_t)row.tokens + 31) / 32) + (uint64_t)(in >> 5);
-        ok = chunk < a.src_chunks;
-    }
-    if (ok) {
-        w0 = a.src_offsets[chunk];
-        const uint64_t w1 = a.src_offsets[chunk + 1];
-        head_words = coset_words(a, n) + rem_words(a, n);
-        ok = w0 <= w1 && w1 <= a.src_cap && w1 - w0 >= head_words && w1 - w0 - head_words < (kMaxUnaryBits / 32u);
-        nu = ok ? (uint32_t)(w1 - w0) - head_words : 0u;
-    }
-    uint32_t ustart = 0, uend = 0;
-    // short chunks of up to four tiles (one-token appends): the lane reads its chunk's plane by itself
-    const bool alone = ok && n <= 4u && nu <= 256u;
-    if (alone) {
+    uint32_t size = 0;
+    if (c < a.n_chunks) {
+        const NewChunk g = new_chunk(a, c);
+        const bool mine = (uint32_t)lane < g.n;
+        // the lane's token in the source; its scale has to be that of the range's first token
+        const int64_t t = g.t0 + (mine ? lane : (int)g.n - 1);
+        const uint64_t at = tab.append_of_token(t), at0 = tab.append_of_token(a.range[g.r].begin);
+        const hq_kv_append_row row = a.src_table[at], ref = a.src_table[at0];
+        const int64_t in = t - row.token0;
+        bool ok = in >= 0 && in < row.tokens && __float_as_uint(row.alpha) == __float_as_uint(ref.alpha) &&
+                  __float_as_uint(row.scale_inv) == __float_as_uint(ref.scale_inv);
+        uint64_t chunk = 0, w0 = 0;
+        uint32_t n = 0, nu = 0, head_words = 0;
+        const uint32_t ti = (uint32_t)in & 31u;
+        if (ok) {
+            const int64_t left = (int64_t)row.tokens - (in & ~INT64_C(31));
+            n = (uint32_t)(left < 32 ? left : 32);
+            chunk = row.first_chunk + (uint64_t)g.h * (uint64_t)(((int64_t)row.tokens + 31) / 32) + (uint64_t)(in >> 5);
+            ok = chunk < a.src_chunks;
+        }
+        if (ok) {
+            w0 = a.src_offsets[chunk];
+            const uint64_t w1 = a.src_offsets[chunk + 1];
+            head_words = coset_words(a, n) + rem_words(a, n);
+            ok = w0 <= w1 && w1 <= a.src_cap && w1 - w0 >= head_words && w1 - w0 - head_words < (kMaxUnaryBits / 32u);
+            nu = ok ? (uint32_t)(w1 - w0) - head_words : 0u;
+        }
+        uint32_t ustart = 0, len = 0;
         const uint32_t *un = a.src_words + w0 + head_words;
-        uint32_t seen = 0;
-        for (uint32_t i = 0; i < nu; i++) {
-            const uint32_t w = __ldg(un + i), p = __popc(w);
-            const uint32_t e0 = 128u * ti, e1 = e0 + 128u;   // terminators before the tile, and up to its last
-            if (seen < e0 && seen + p >= e0) {
-                uint32_t x = w;
-                for (uint32_t d = e0 - 1u - seen; d; d--) x &= x - 1u;
-                ustart = i * 32u + (uint32_t)__ffs((int)x);
-            }
-            if (seen < e1 && seen + p >= e1) {
-                uint32_t x = w;
-                for (uint32_t d = e1 - 1u - seen; d; d--) x &= x - 1u;
-                uend = i * 32u + (uint32_t)__ffs((int)x);
-            }
-            seen += p;
-        }
-        ok = seen == 128u * n;
-    }
-    // larger ones: the warp reads each distinct chunk once
-    unsigned todo = __ballot_sync(0xffffffffu, ok && !alone);
-    while (todo) {
-        const int lead = __ffs((int)todo) - 1;
-        const uint64_t lc = __shfl_sync(0xffffffffu, (unsigned long long)chunk, lead);
-        const uint64_t lw = __shfl_sync(0xffffffffu, (unsigned long long)(w0 + head_words), lead);
-        const uint32_t ln = __shfl_sync(0xffffffffu, n, lead), lu = __shfl_sync(0xffffffffu, nu, lead);
-        const bool good = tile_starts(a.src_words + lw, lu, ln, starts[warp], lane);
-        const bool mine = ok && !alone && chunk == lc;
-        if (mine) {
-            if (good) {
-                ustart = starts[warp][ti];
-                uend = starts[warp][ti + 1];
-            } else {
-                ok = false;
-            }
-        }
-        todo &= ~__ballot_sync(0xffffffffu, mine || (todo >> lane & 1u && chunk == lc));
-        __syncwarp();
-    }
-    // a tile that is not there, or not sound, becomes one of zero symbols (128 terminators)
-    uint32_t len = ok ? uend - ustart : 128u;
-    unsigned long long bits = (uint32_t)lane < g.n ? len : 0u;
+        // every tile of one source chunk: the new chunk is that chunk
+        const uint64_t c0 = __shfl_sync(0xffffffffu, (unsigned long long)chunk, 0);
+        bool whole = __all_sync(0xffffffffu, ok && chunk == c0 && n == g.n && (!mine || ti == (uint32_t)lane));
+        if (whole) {
+            uint32_t ones = 0;
+            for (uint32_t i0 = 0; i0 < nu; i0 += 256) {
+                uint32_t w[8];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) bits += __shfl_xor_sync(0xffffffffu, bits, o);
-    if (bits >= kMaxUnaryBits) {   // tiles of enormous symbols that together exceed what a chunk may hold
-        ok = false;
-        len = 128u;
-        bits = 128ull * g.n;
+                for (int u = 0; u < 8; u++) w[u] = i0 + 32u * u + lane < nu ? __ldg(un + i0 + 32u * u + lane) : 0u;
+#pragma unroll
+                for (int u = 0; u < 8; u++) ones += __popc(w[u]);
+            }
+            ones = __reduce_add_sync(0xffffffffu, ones);
+            const uint32_t last = nu ? __ldg(un + nu - 1) : 0u;
+            whole = ones == 128u * n && last != 0u;   // else found out tile by tile
+            if (whole && lane == 0) len = nu * 32u - (uint32_t)__clz((int)last);   // lane 0's run is the chunk's
+        }
+        if (!whole) {
+            // a tile in a chunk of its own
+            const bool alone = ok && n == 1u && nu <= 256u;
+            if (alone) {
+                uint32_t ones = 0, last = 0;
+                for (uint32_t i0 = 0; i0 < nu; i0 += 8) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int u = 0; u < 8; u++) w[u] = i0 + u < nu ? __ldg(un + i0 + u) : 0u;
+#pragma unroll
+                    for (int u = 0; u < 8; u++) {
+                        ones += __popc(w[u]);
+                        if (w[u]) last = (i0 + u) * 32u + 32u - (uint32_t)__clz((int)w[u]);
+                    }
+                }
+                ok = ones == 128u;
+                len = last;
+            }
+            // larger ones: the warp reads each distinct chunk once
+            unsigned todo = __ballot_sync(0xffffffffu, ok && !alone);
+            while (todo) {
+                const int lead = __ffs((int)todo) - 1;
+                const uint64_t lc = __shfl_sync(0xffffffffu, (unsigned long long)chunk, lead);
+                const uint64_t lw = __shfl_sync(0xffffffffu, (unsigned long long)(w0 + head_words), lead);
+                const uint32_t ln = __shfl_sync(0xffffffffu, n, lead), lu = __shfl_sync(0xffffffffu, nu, lead);
+                const bool good = tile_starts(a.src_words + lw, lu, ln, starts[warp], lane);
+                const bool here = ok && !alone && chunk == lc;
+                if (here) {
+                    if (good) {
+                        ustart = starts[warp][ti];
+                        len = starts[warp][ti + 1] - ustart;
+                    } else {
+                        ok = false;
+                    }
+                }
+                todo &= ~__ballot_sync(0xffffffffu, here);
+            }
+            // a tile that is not there, or not sound, becomes one of zero symbols (128 terminators)
+            if (!ok) {
+                ustart = 0;
+                len = 128u;
+            }
+        }
+        unsigned long long bits = mine ? len : 0u;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) bits += __shfl_xor_sync(0xffffffffu, bits, o);
+        if (bits >= kMaxUnaryBits) {   // tiles of enormous symbols that together exceed what a chunk may hold
+            ok = false;
+            ustart = 0;
+            len = 128u;
+            bits = 128ull * g.n;
+        }
+        const uint64_t tag = ok ? w0 | (uint64_t)ti << 48 | (uint64_t)n << 56 : 0ull;
+        if (mine) a.tiles[c * 32 + lane] = make_uint4((uint32_t)tag, (uint32_t)(tag >> 32), ustart, len);
+        size = coset_words(a, g.n) + rem_words(a, g.n) + (uint32_t)((bits + 31) >> 5);
+        if (lane == 0) a.sizes[c] = size;
     }
-    const uint64_t tag = ok ? w0 | (uint64_t)ti << 48 | (uint64_t)n << 56 : 0ull;
-    if ((uint32_t)lane < g.n) a.tiles[c * 32 + lane] = make_uint4((uint32_t)tag, (uint32_t)(tag >> 32), ustart, len);
-    if (lane == 0) a.sizes[c] = coset_words(a, g.n) + rem_words(a, g.n) + (uint32_t)((bits + 31) >> 5);
+    if (lane == 0) size_of[warp] = size;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        uint64_t sum = 0;
+        for (int i = 0; i < kRepackWarps; i++) sum += size_of[i];
+        a.sums[blockIdx.x] = sum;
+    }
 }
 
 // Sum over the CTA of one value per thread; the same in all.
@@ -248,18 +286,55 @@ __device__ __forceinline__ unsigned long long cta_sum(unsigned long long v, unsi
     return v;
 }
 
+// One plane of a new chunk: `words` words at dst (of which those below `room` exist), of runs whose first bits
+// are at[r] (at[runs] the end) and come from absolute source bit from[r] on (kNoSource: `fill` instead).
+constexpr unsigned long long kNoSource = ~0ull;
+__device__ __forceinline__ uint32_t run_bits(const RepackArgs &a, unsigned long long from, uint32_t skip, uint32_t need,
+                                             uint32_t fill) {
+    return from == kNoSource ? fill : stream_bits(a.src_words, from + skip, need);
+}
+__device__ __forceinline__ void copy_plane(const RepackArgs &a, uint32_t *dst, uint64_t room, uint32_t words,
+                                           const unsigned long long *from, const uint32_t *at, int runs, uint32_t fill,
+                                           int lane) {
+#pragma unroll 4
+    for (uint32_t i = lane; i < words; i += 32) {
+        const uint32_t b = 32u * i;
+        int r = 0;
+        if (runs > 1) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                if (r + o < runs && at[r + o] <= b) r += o;
+        }
+        const uint32_t left = at[r + 1] - b, have = min(32u, left);
+        uint32_t v = run_bits(a, from[r], b - at[r], have, fill);
+        if (have < 32u) {
+            v &= (1u << have) - 1u;
+            if (r + 1 < runs) {
+                // the next run's first bits (its end may lie in this word too: bits behind it are the plane's
+                // padding, or of a third run, which no plane has)
+                const uint32_t more = min(32u - have, at[r + 2] - at[r + 1]);
+                uint32_t x = run_bits(a, from[r + 1], 0u, more, fill);
+                if (more < 32u) x &= (1u << more) - 1u;
+                v |= x << have;
+            }
+        }
+        if (i < room) dst[i] = v;
+    }
+}
+
 __global__ void __launch_bounds__(kRepackWarps * 32) repack_copy(const __grid_constant__ RepackArgs a) {
     __shared__ unsigned long long tmp[kRepackWarps];
-    __shared__ unsigned long long src[kRepackWarps][32];   // first word of each tile's source chunk
-    __shared__ uint32_t info[kRepackWarps][32];            // tile | its chunk's tiles << 8 (0: zero symbols)
-    __shared__ uint32_t from[kRepackWarps][32];            // its first unary bit there
-    __shared__ uint32_t at[kRepackWarps][33];              // and in the new plane
+    __shared__ unsigned long long from[kRepackWarps][3][32];   // first source bit of each run, by plane
+    __shared__ uint32_t at[kRepackWarps][3][34];               // and its first bit in the new plane
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint64_t per = (a.n_chunks + gridDim.x - 1) / gridDim.x;
-    const uint64_t c0 = per * blockIdx.x, c1 = min(a.n_chunks, c0 + per);
+    // whole blocks of the first launch
+    const uint64_t blocks = (a.n_chunks + kRepackWarps - 1) / kRepackWarps;
+    const uint64_t b0 = blocks * blockIdx.x / gridDim.x, b1 = blocks * (blockIdx.x + 1) / gridDim.x;
+    const uint64_t c0 = b0 * kRepackWarps, c1 = min(a.n_chunks, b1 * kRepackWarps);
+    cudaGridDependencySynchronize();
     if (c0 >= c1) return;
     unsigned long long before = 0;
-    for (uint64_t i = threadIdx.x; i < c0; i += blockDim.x) before += a.sizes[i];
+    for (uint64_t i = threadIdx.x; i < b0; i += blockDim.x) before += a.sums[i];
     unsigned long long base = cta_sum(before, tmp);
     unsigned long long payload = 0;
     uint32_t status = 0;
@@ -282,77 +357,47 @@ __global__ void __launch_bounds__(kRepackWarps * 32) repack_copy(const __grid_co
         const bool mine = (uint32_t)lane < g.n;
         uint4 d = make_uint4(0u, 0u, 0u, 0u);
         if (mine) d = a.tiles[c * 32 + lane];
-        uint32_t incl = mine ? d.w : 0u;
+        uint32_t incl = d.w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
         }
-        src[warp][lane] = ((unsigned long long)(d.y & 0xFFFFu) << 32) | d.x;
-        info[warp][lane] = ((d.y >> 16) & 0xFFu) | ((d.y >> 24) << 8);
-        from[warp][lane] = d.z;
-        at[warp][lane + 1] = incl;
-        if (lane == 0) at[warp][0] = 0;
-        __syncwarp();
-        if (mine && (d.y >> 24) == 0) status |= HQ_ST_CORRUPT;
-        const uint32_t nbits = at[warp][32];
-        if (lane == 0) payload += (unsigned long long)nbits + g.n * (a.rem_bits + (a.e8 ? 16u : 0u));
+        const uint32_t nbits = __shfl_sync(0xffffffffu, incl, 31);
+        // runs: a tile that does not follow the one before it in one source chunk starts one
+        const uint32_t px = __shfl_up_sync(0xffffffffu, d.x, 1), py = __shfl_up_sync(0xffffffffu, d.y, 1);
+        const uint32_t n = d.y >> 24, ti = (d.y >> 16) & 0xFFu;
+        const bool first = mine && (lane == 0 || n == 0u || px != d.x || d.y != py + 0x10000u);
+        const unsigned heads = __ballot_sync(0xffffffffu, first);
+        const int runs = __popc(heads);
         const uint32_t nc = coset_words(a, g.n), nr = rem_words(a, g.n), nu = (nbits + 31u) >> 5;
-        const uint32_t total = nc + nr + nu;
-        if (lane == 0) a.offsets[c] = w0;
-        for (uint32_t i = lane; i < total; i += 32) {
-            uint32_t v = 0;
-            if (i < nc) {
-#pragma unroll
-                for (int u = 0; u < 2; u++) {
-                    const uint32_t t = 2u * i + u;
-                    const uint32_t f = t < g.n ? info[warp][t] : 0u;
-                    if (f) v |= (stream_bits(a.src_words, src[warp][t] * 32 + 16u * (f & 0xFFu), 16u) & 0xFFFFu)
-                                << (16 * u);
-                }
-            } else if (i < nc + nr) {
-                const uint32_t b = 32u * (i - nc), t = b / a.rem_bits, skip = b - t * a.rem_bits;
-                const uint32_t have = min(32u, a.rem_bits - skip);
-                uint32_t f = info[warp][t];
-                if (f) {
-                    const uint64_t s = (src[warp][t] + coset_words(a, f >> 8)) * 32 + (uint64_t)(f & 0xFFu) * a.rem_bits;
-                    v = stream_bits(a.src_words, s + skip, have);
-                    if (have < 32u) v &= (1u << have) - 1u;
-                }
-                if (have < 32u && t + 1 < g.n && (f = info[warp][t + 1])) {
-                    const uint64_t s =
-                        (src[warp][t + 1] + coset_words(a, f >> 8)) * 32 + (uint64_t)(f & 0xFFu) * a.rem_bits;
-                    v |= stream_bits(a.src_words, s, 32u - have) << have;
-                }
-            } else {
-                const uint32_t b = 32u * (i - nc - nr);
-                uint32_t t = 0;
-#pragma unroll
-                for (int o = 16; o; o >>= 1)
-                    if (t + o < g.n && at[warp][t + o] <= b) t += o;
-                const uint32_t skip = b - at[warp][t];
-                const uint32_t have = min(32u, at[warp][t + 1] - b);
-                uint32_t f = info[warp][t];
-                v = 0xFFFFFFFFu;
-                if (f)
-                    v = stream_bits(a.src_words,
-                                    (src[warp][t] + coset_words(a, f >> 8) + rem_words(a, f >> 8)) * 32 +
-                                        from[warp][t] + skip, have);
-                if (have < 32u) {
-                    v &= (1u << have) - 1u;
-                    if (t + 1 < g.n) {
-                        f = info[warp][t + 1];
-                        uint32_t x = 0xFFFFFFFFu;
-                        if (f)
-                            x = stream_bits(a.src_words,
-                                            (src[warp][t + 1] + coset_words(a, f >> 8) + rem_words(a, f >> 8)) * 32 +
-                                                from[warp][t + 1], 32u - have);
-                        v |= x << have;
-                    }
-                }
-            }
-            if (w0 + i < a.cap) a.words[w0 + i] = v;
+        if (first) {
+            const int r = __popc(heads & ((1u << lane) - 1u));
+            const unsigned long long src = (unsigned long long)(d.y & 0xFFFFu) << 32 | d.x;
+            const uint32_t snc = coset_words(a, n), snr = rem_words(a, n);
+            from[warp][0][r] = n ? src * 32 + 16u * ti : kNoSource;
+            from[warp][1][r] = n ? (src + snc) * 32 + (unsigned long long)ti * a.rem_bits : kNoSource;
+            from[warp][2][r] = n ? (src + snc + snr) * 32 + d.z : kNoSource;
+            at[warp][0][r] = 16u * lane;
+            at[warp][1][r] = a.rem_bits * lane;
+            at[warp][2][r] = incl - d.w;
         }
+        if (lane == 0) {
+            at[warp][0][runs] = 16u * g.n;
+            at[warp][1][runs] = a.rem_bits * g.n;
+            at[warp][2][runs] = nbits;
+            a.offsets[c] = w0;
+            payload += (unsigned long long)nbits + g.n * (a.rem_bits + (a.e8 ? 16u : 0u));
+        }
+        __syncwarp();
+        if (mine && n == 0u) status |= HQ_ST_CORRUPT;
+        // words of this chunk that the buffer has room for
+        const uint64_t room = w0 < a.cap ? a.cap - w0 : 0ull;
+        uint32_t *const dst = a.words + w0;
+        copy_plane(a, dst, room, nc, from[warp][0], at[warp][0], runs, 0u, lane);
+        copy_plane(a, dst + nc, room > nc ? room - nc : 0ull, nr, from[warp][1], at[warp][1], runs, 0u, lane);
+        copy_plane(a, dst + nc + nr, room > nc + nr ? room - nc - nr : 0ull, nu, from[warp][2], at[warp][2], runs, ~0u, lane);
+        const uint32_t total = nc + nr + nu;
         if (w0 + total > a.cap) status |= HQ_ST_CAPACITY;
         if (c + 1 == a.n_chunks && lane == 0) {
             a.offsets[c + 1] = w0 + total;
@@ -401,7 +446,9 @@ extern "C" int hq_kv_repack_workspace_bytes(int32_t heads, const int64_t *h_rang
     const int64_t c = chunks_of_ranges(heads, h_ranges, n_ranges, INT64_MAX);
     if (c < 0) return HQ_EINVAL;
     if (c > (INT64_C(1) << 31)) return HQ_EUNSUPPORTED;
-    *bytes = ((size_t)c * (32 * sizeof(uint4) + sizeof(uint32_t)) + 255) & ~(size_t)255;
+    // tiles, sums by CTA, sizes
+    *bytes = ((size_t)c * (32 * sizeof(uint4) + sizeof(uint32_t)) + ((size_t)c / kRepackWarps + 1) * sizeof(uint64_t) + 255) &
+             ~(size_t)255;
     return HQ_OK;
 }
 
@@ -454,7 +501,8 @@ extern "C" int hq_kv_repack(const hq_kv_cache *src, hq_kv_cache *dst, const int6
     a.tail = dst->d_tail;
     a.stats = dst->d_stats;
     a.tiles = (uint4 *)workspace;
-    a.sizes = (uint32_t *)((char *)workspace + (size_t)chunks * 32 * sizeof(uint4));
+    a.sums = (uint64_t *)((char *)workspace + (size_t)chunks * 32 * sizeof(uint4));
+    a.sizes = (uint32_t *)(a.sums + chunks / kRepackWarps + 1);
     a.n_chunks = (uint64_t)chunks;
     a.heads = src->heads;
     a.n_ranges = n_ranges;
@@ -469,10 +517,18 @@ extern "C" int hq_kv_repack(const hq_kv_cache *src, hq_kv_cache *dst, const int6
     const uint64_t ctas = (a.n_chunks + kRepackWarps - 1) / kRepackWarps;
     repack_measure<<<(unsigned)ctas, kRepackWarps * 32, 0, s>>>(a);
     if (cudaGetLastError() != cudaSuccess) return HQ_ECUDA;
-    // all resident at once (8 CTAs of 256 threads per SM): each sums the sizes before its own chunks
-    const uint64_t most = 148 * 8;
-    repack_copy<<<(unsigned)(ctas < most ? ctas : most), kRepackWarps * 32, 0, s>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return HQ_ECUDA;
+    // all resident at once (16 CTAs of 128 threads per SM): each sums the sizes before its own chunks
+    const uint64_t most = 148 * 16;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ctas < most ? ctas : most));
+    cfg.blockDim = dim3(kRepackWarps * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, repack_copy, a) != cudaSuccess) return HQ_ECUDA;
     dst->tokens = h_ranges[2 * n_ranges - 1];
     dst->chunks = (uint64_t)chunks;
     dst->appends = (uint64_t)n_ranges;
