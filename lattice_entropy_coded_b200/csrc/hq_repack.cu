@@ -293,32 +293,76 @@ __device__ __forceinline__ uint32_t run_bits(const RepackArgs &a, unsigned long 
                                              uint32_t fill) {
     return from == kNoSource ? fill : stream_bits(a.src_words, from + skip, need);
 }
+// Word i, from the run that holds its first bit and the one after it.
+__device__ __forceinline__ uint32_t plane_word(const RepackArgs &a, uint32_t i, const unsigned long long *from,
+                                               const uint32_t *at, int runs, uint32_t fill) {
+    const uint32_t b = 32u * i;
+    int r = 0;
+    if (runs > 1) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            if (r + o < runs && at[r + o] <= b) r += o;
+    }
+    const uint32_t left = at[r + 1] - b, have = min(32u, left);
+    uint32_t v = run_bits(a, from[r], b - at[r], have, fill);
+    if (have < 32u) {
+        v &= (1u << have) - 1u;
+        if (r + 1 < runs) {
+            // the next run's first bits (its end may lie in this word too: bits behind it are the plane's
+            // padding, or of a third run, which no plane has)
+            const uint32_t more = min(32u - have, at[r + 2] - at[r + 1]);
+            uint32_t x = run_bits(a, from[r + 1], 0u, more, fill);
+            if (more < 32u) x &= (1u << more) - 1u;
+            v |= x << have;
+        }
+    }
+    return v;
+}
+// Words [i0, i1) of a plane, 32 bits of the source from bit b on each: a word to a lane, eight in flight.
+__device__ __forceinline__ void copy_run(const uint32_t *words, uint32_t *dst, uint32_t i0, uint32_t i1,
+                                         unsigned long long b, int lane) {
+    const uint32_t *p = words + (b >> 5);
+    const uint32_t sh = (uint32_t)b & 31u, n = i1 - i0;
+    dst += i0;
+    for (uint32_t k0 = lane; k0 < n; k0 += 256) {
+        uint32_t lo[8], hi[8];
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+            const uint32_t k = k0 + 32u * u;
+            lo[u] = k < n ? __ldg(p + k) : 0u;
+            hi[u] = sh && k < n ? __ldg(p + k + 1) : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; u++)
+            if (k0 + 32u * u < n) dst[k0 + 32u * u] = __funnelshift_r(lo[u], hi[u], sh);
+    }
+}
+constexpr int kFewRuns = 8;   // up to which a plane's whole words are copied run by run
 __device__ __forceinline__ void copy_plane(const RepackArgs &a, uint32_t *dst, uint64_t room, uint32_t words,
                                            const unsigned long long *from, const uint32_t *at, int runs, uint32_t fill,
                                            int lane) {
+    if (words == 0) return;
+    if (runs > kFewRuns || room < words) {
 #pragma unroll 4
-    for (uint32_t i = lane; i < words; i += 32) {
-        const uint32_t b = 32u * i;
-        int r = 0;
-        if (runs > 1) {
-#pragma unroll
-            for (int o = 16; o; o >>= 1)
-                if (r + o < runs && at[r + o] <= b) r += o;
+        for (uint32_t i = lane; i < words; i += 32) {
+            const uint32_t v = plane_word(a, i, from, at, runs, fill);
+            if (i < room) dst[i] = v;
         }
-        const uint32_t left = at[r + 1] - b, have = min(32u, left);
-        uint32_t v = run_bits(a, from[r], b - at[r], have, fill);
-        if (have < 32u) {
-            v &= (1u << have) - 1u;
-            if (r + 1 < runs) {
-                // the next run's first bits (its end may lie in this word too: bits behind it are the plane's
-                // padding, or of a third run, which no plane has)
-                const uint32_t more = min(32u - have, at[r + 2] - at[r + 1]);
-                uint32_t x = run_bits(a, from[r + 1], 0u, more, fill);
-                if (more < 32u) x &= (1u << more) - 1u;
-                v |= x << have;
-            }
+        return;
+    }
+    for (int r = 0; r < runs; r++) {
+        const uint32_t i0 = (at[r] + 31u) >> 5, i1 = at[r + 1] >> 5;   // the words that lie in the run alone
+        if (i0 >= i1) continue;
+        if (from[r] == kNoSource) {
+            for (uint32_t i = i0 + lane; i < i1; i += 32) dst[i] = fill;
+        } else {
+            copy_run(a.src_words, dst, i0, i1, from[r] + (32u * i0 - at[r]), lane);
         }
-        if (i < room) dst[i] = v;
+    }
+    // the words that runs end in
+    if (lane < runs && (at[lane + 1] & 31u)) {
+        const uint32_t i = at[lane + 1] >> 5;
+        dst[i] = plane_word(a, i, from, at, runs, fill);
     }
 }
 
@@ -391,13 +435,21 @@ __global__ void __launch_bounds__(kRepackWarps * 32) repack_copy(const __grid_co
         }
         __syncwarp();
         if (mine && n == 0u) status |= HQ_ST_CORRUPT;
+        const uint32_t total = nc + nr + nu;
         // words of this chunk that the buffer has room for
         const uint64_t room = w0 < a.cap ? a.cap - w0 : 0ull;
         uint32_t *const dst = a.words + w0;
-        copy_plane(a, dst, room, nc, from[warp][0], at[warp][0], runs, 0u, lane);
-        copy_plane(a, dst + nc, room > nc ? room - nc : 0ull, nr, from[warp][1], at[warp][1], runs, 0u, lane);
-        copy_plane(a, dst + nc + nr, room > nc + nr ? room - nc - nr : 0ull, nu, from[warp][2], at[warp][2], runs, ~0u, lane);
-        const uint32_t total = nc + nr + nu;
+        // all tiles of a source chunk: its words as they are
+        const bool whole = runs == 1 && __shfl_sync(0xffffffffu, n == g.n && ti == 0u, 0);
+        if (whole && room >= total) {
+            copy_run(a.src_words, dst, 0u, total, ((unsigned long long)(__shfl_sync(0xffffffffu, d.y, 0) & 0xFFFFu) << 32 |
+                                                   __shfl_sync(0xffffffffu, d.x, 0)) * 32ull, lane);
+        } else {
+            copy_plane(a, dst, room, nc, from[warp][0], at[warp][0], runs, 0u, lane);
+            copy_plane(a, dst + nc, room > nc ? room - nc : 0ull, nr, from[warp][1], at[warp][1], runs, 0u, lane);
+            copy_plane(a, dst + nc + nr, room > nc + nr ? room - nc - nr : 0ull, nu, from[warp][2], at[warp][2], runs, ~0u,
+                       lane);
+        }
         if (w0 + total > a.cap) status |= HQ_ST_CAPACITY;
         if (c + 1 == a.n_chunks && lane == 0) {
             a.offsets[c + 1] = w0 + total;
