@@ -161,20 +161,22 @@ struct Piece {
 
 // ------------------------------------------------------------------ E8 dither
 // d = w - Q(w) of dither_block<HQ_E8>, bit for bit, in one pass over both candidates.  With w uniform
-// on [0, 4)^8, let c_i be w_i's residual to the nearest even integer (candidate A) and a_i = |c_i|;
-// the one to the nearest odd integer (candidate B) is c_i - sign(c_i), of size 1 - a_i.  The squared
-// distances' difference is then linear in the a_i:
-//   D = (|w - A|^2 - |w - B|^2) / 2 = sum a - 4 + 2 p_A (1 - max a) - 2 p_B min a,
+// on [0, 4)^8, let c_i be w_i's residual to the nearest odd integer (candidate B) and b_i = |c_i|; the
+// one to the nearest even integer (candidate A) is c_i - sign(c_i), of size 1 - b_i.  The squared
+// distances' difference is then linear in the b_i:
+//   D = (|w - A|^2 - |w - B|^2) / 2 = 4 - sum b + 2 p_A min b - 2 p_B (1 - max b),
 // the last terms being the parity fixes (the largest residual r becomes 2 - r), with the parities of
 // the rounded halves from the two top bits of each w: p_B the XOR of the "w >= 2", p_A of the
 // "1 <= w < 3".  Everything is exact in units of 2^-22 but the sum (within 16 units).  The reading
 // compares fp32 distances, which are off by less than 2^-16 here (the bound at Lattice<HQ_E8>): a
-// difference within 2^-12, a coordinate on a rounding border (a = 0 or 1) or two equal largest
+// difference within 2^-12, a coordinate on a rounding border (b = 0 or 1) or two equal largest
 // residuals under a fix goes to the reading's own code instead, about one block in 4000.
 //
-// Bound by the ALU pipe (half the FMA pipe's rate), so the conversions run on the XU pipe and the
-// search for the largest residual on the FMA pipe: with sizes in whole units,
-// saturate(size + 1 - largest) is 1 at the largest and 0 elsewhere.
+// Bound by the ALU pipe (half the FMA pipe's rate), so what can be is put on the FMA pipe: w mod 2 by
+// one mad.hi that also sets the exponent, and the search for the largest residual by
+// saturate(size + 1 - largest), 1 at the largest and 0 elsewhere as sizes are whole units.  24.8
+// lane-instructions per element, 11.3 of them the hash, 59.5 us for 67 million elements alone
+// (dither_block: about 34).
 constexpr float kDitherUnit = 4194304.0f;       // 2^22: d is returned in units of 2^-22
 constexpr uint64_t kSplitGolden = 0x9E3779B97F4A7C15ull;
 
@@ -208,8 +210,16 @@ __device__ __forceinline__ float add_sat(float a, float b) {
     return r;
 }
 
+// bits 8..30 of x (w mod 2 in units of 2^-22) plus 2^23, as a float
+__device__ __forceinline__ float frac2(uint32_t x) {
+    uint32_t r;
+    asm("mad.hi.u32 %0, %1, %2, %3;" : "=r"(r) : "r"(x * 2u), "r"(1u << 23), "r"(0x4B000000u));
+    return __uint_as_float(r);
+}
+
 // The block whose first pair has generator state z0; d in units of 2^-22.
 __device__ __forceinline__ void e8_dither(uint64_t z0, float (&d)[8]) {
+    constexpr float U = kDitherUnit;
     float c[8];
     uint32_t xe = 0, xo = 0;
 #pragma unroll
@@ -218,11 +228,10 @@ __device__ __forceinline__ void e8_dither(uint64_t z0, float (&d)[8]) {
         dither_pair(z0 + (uint64_t)i * kSplitGolden, x, y);
         xe ^= x;
         xo ^= y;
-        // w mod 2 as a signed fraction: bits 8..30, the border 1 being the lower end
-        c[2 * i] = (float)(int32_t)((x & 0x7FFFFF00u) * 2u);
-        c[2 * i + 1] = (float)(int32_t)((y & 0x7FFFFF00u) * 2u);
+        const float2 r = f2_sub(make_float2(frac2(x), frac2(y)), make_float2(8388608.0f + U, 8388608.0f + U));
+        c[2 * i] = r.x;
+        c[2 * i + 1] = r.y;
     }
-    constexpr float U = 2147483648.0f;          // here a unit of w is 2^31; sizes are multiples of 2^9
     const uint32_t par = xe ^ xo;
     const bool pb = (int32_t)par < 0, pa = (int32_t)(par ^ (par << 1)) < 0;
     float lo = fabsf(c[0]), hi = lo;
@@ -233,29 +242,23 @@ __device__ __forceinline__ void e8_dither(uint64_t z0, float (&d)[8]) {
     }
     const float s0 = __fadd_rn(__fadd_rn(fabsf(c[0]), fabsf(c[1])), __fadd_rn(fabsf(c[2]), fabsf(c[3])));
     const float s1 = __fadd_rn(__fadd_rn(fabsf(c[4]), fabsf(c[5])), __fadd_rn(fabsf(c[6]), fabsf(c[7])));
-    const float diff = __fadd_rn(__fadd_rn(__fsub_rn(s0, 4.0f * U), s1),
-                                 __fsub_rn(pa ? __fmaf_rn(-2.0f, hi, 2.0f * U) : 0.0f, pb ? __fadd_rn(lo, lo) : 0.0f));
+    const float diff = __fadd_rn(__fsub_rn(__fsub_rn(4.0f * U, s0), s1),
+                                 __fsub_rn(pa ? __fadd_rn(lo, lo) : 0.0f, pb ? __fmaf_rn(-2.0f, hi, 2.0f * U) : 0.0f));
     const bool odd = diff > 0.0f, fix = odd ? pb : pa;
-    // sizes with B's sign turned: |c| - m0; the fix takes the largest by 2 the other way
-    const float m0 = odd ? -U : 0.0f, turn = odd ? 2.0f * kDitherUnit : -2.0f * kDitherUnit;
-    const float top = odd ? __fsub_rn(U, lo) : hi;
-    const float shift = fix ? __fsub_rn(1.0f, __fmul_rn(top, 0x1p-9f)) : -INFINITY;
-    float e[8], t[8];
+    // signed sizes |c| - m (A's turned); the fix takes the largest by 2 the other way
+    const float m = odd ? 0.0f : -U, turn = odd ? -2.0f * U : 2.0f * U, top = odd ? hi : __fsub_rn(U, lo);
+    const float shift = fix ? __fsub_rn(1.0f, top) : -INFINITY;
     float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        t[i] = __fmul_rn(__fadd_rn(fabsf(c[i]), m0), 0x1p-9f);
-        e[i] = add_sat(fabsf(t[i]), shift);
-    }
-#pragma unroll
     for (int i = 0; i < 4; i++) {
-        const float2 e2 = make_float2(e[2 * i], e[2 * i + 1]);
-        sum = f2_add(sum, e2);
-        const float2 r = f2_fma(e2, make_float2(turn, turn), make_float2(t[2 * i], t[2 * i + 1]));
+        const float t0 = __fadd_rn(fabsf(c[2 * i]), m), t1 = __fadd_rn(fabsf(c[2 * i + 1]), m);
+        const float2 e = make_float2(add_sat(fabsf(t0), shift), add_sat(fabsf(t1), shift));
+        sum = f2_add(sum, e);
+        const float2 r = f2_fma(e, make_float2(turn, turn), make_float2(t0, t1));
         d[2 * i] = __uint_as_float(__float_as_uint(r.x) ^ (__float_as_uint(c[2 * i]) & 0x80000000u));
         d[2 * i + 1] = __uint_as_float(__float_as_uint(r.y) ^ (__float_as_uint(c[2 * i + 1]) & 0x80000000u));
     }
-    if (fabsf(diff) <= 0x1p-12f * U || lo == 0.0f || hi == U || __fadd_rn(sum.x, sum.y) != (fix ? 1.0f : 0.0f)) {
+    if (fabsf(diff) <= 1024.0f || lo == 0.0f || hi == U || __fadd_rn(sum.x, sum.y) != (fix ? 1.0f : 0.0f)) {
         float r[8];
         e8_dither_reading(z0, r);
 #pragma unroll
@@ -267,18 +270,37 @@ __device__ __forceinline__ void e8_dither(uint64_t z0, float (&d)[8]) {
 // Forms of the Rice code: no remainders at all (k = 0: the 2-bit caches), or any parameters.
 enum AttnForm { kFormUnary = 0, kFormGeneral = 1 };
 
-// Unary pairs of E8 at k = 0: the next 10 stream bits -> both codewords.  Bits 0..4 their length,
-// byte 1 and byte 2 the two codes 2 m + 128 (2 m the zigzag inverse doubled), bit 24 the parity of
-// m of both, bit 25 of the first, bit 31 set if both codewords end inside the 10 bits (one pair in
-// 2000 does not at 2 bits per scalar).
+// Codewords two at a time: the next 10 unary bits -> both quotients.  Bits 0..4 their length, byte 1 and
+// byte 2 the quotients, bit 31 set if both end inside the 10 bits (at 2 bits per scalar one pair in 2000
+// does not).  CODES (E8 without remainders): bytes 1 and 2 are the codes 2 m + 128 instead (2 m the zigzag
+// inverse doubled), bit 24 the parity of m of both, bit 25 of the first.
 constexpr int kPairBits = 10;
+template <bool CODES>
 __device__ __forceinline__ uint32_t pair_entry(uint32_t w) {
     const uint32_t t0 = (uint32_t)__ffs((int)(w | 0x80000000u)) - 1u;
     const uint32_t t1 = t0 < 31u ? (uint32_t)__ffs((int)((w >> (t0 + 1u)) | 0x80000000u)) - 1u : 31u;
     if (t0 + t1 + 2u > (uint32_t)kPairBits) return 0u;
+    if (!CODES) return 0x80000000u | (t0 + t1 + 2u) | t0 << 8 | t1 << 16;
     const uint32_t a = t0 ^ (0u - (t0 & 1u)), b = t1 ^ (0u - (t1 & 1u));   // 2 m
     return 0x80000000u | (t0 + t1 + 2u) | ((a + 128u) & 0xFFu) << 8 | ((b + 128u) & 0xFFu) << 16 |
            (((a ^ b) >> 1) & 1u) << 24 | ((a >> 1) & 1u) << 25;
+}
+// Four pairs from unary bit bp on; whether all of them ended in time, and their length.  The plane's
+// terminators were counted, so a lane's codewords end inside it (or in the pad behind its last word,
+// which the second word of a window may reach).
+__device__ __forceinline__ bool read_pairs(const uint32_t *un, uint32_t bp, const uint32_t *pairs, uint32_t (&e)[4],
+                                           uint32_t &used) {
+    used = 0;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const uint32_t *p = un + ((bp + used) >> 5);
+        uint32_t x = __funnelshift_r(p[0], p[1], bp + used);
+        e[2 * h] = pairs[x & ((1u << kPairBits) - 1u)];
+        x = __funnelshift_r(x, 0u, e[2 * h]);
+        e[2 * h + 1] = pairs[x & ((1u << kPairBits) - 1u)];
+        used += (e[2 * h] + e[2 * h + 1]) & 0x1Fu;
+    }
+    return (int32_t)(e[0] & e[1] & e[2] & e[3]) < 0;
 }
 
 // What a lane decodes in a round: its quarter of a tile, 32 codes in four blocks of 8.
@@ -317,19 +339,8 @@ __device__ __forceinline__ void decode_block(Quarter &t, int k, int kl, uint64_t
     const uint32_t c = t.coset & 1u;
     t.coset >>= 1;
     if constexpr (LAT == HQ_E8 && FORM == kFormUnary && STAGED) {
-        // The plane's terminators were counted, so a lane's 32 codewords end inside it (or in the pad
-        // behind its last word, which the second word of a window may reach).
-        uint32_t e[4], used = 0;
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const uint32_t *p = t.un + ((t.bp + used) >> 5);
-            uint32_t x = __funnelshift_r(p[0], p[1], t.bp + used);
-            e[2 * h] = pairs[x & ((1u << kPairBits) - 1u)];
-            x = __funnelshift_r(x, 0u, e[2 * h]);
-            e[2 * h + 1] = pairs[x & ((1u << kPairBits) - 1u)];
-            used += (e[2 * h] + e[2 * h + 1]) & 0x1Fu;
-        }
-        if ((int32_t)(e[0] & e[1] & e[2] & e[3]) < 0) {
+        uint32_t e[4], used;
+        if (read_pairs(t.un, t.bp, pairs, e, used)) {
             t.bp += used;
             // the stripped parity of m_7: that of m_0 .. m_6
             const uint32_t p7 = ((e[0] ^ e[1] ^ e[2]) >> 24 ^ e[3] >> 25) & 1u;
@@ -355,8 +366,18 @@ __device__ __forceinline__ void decode_block(Quarter &t, int k, int kl, uint64_t
         }
     } else {
         uint32_t qv[8], rv[8];
-        unary4<STAGED>(t.un, t.nu, t.bp, t.ok, qv);
-        unary4<STAGED>(t.un, t.nu, t.bp, t.ok, qv + 4);
+        uint32_t e[4], used;
+        if (STAGED && read_pairs(t.un, t.bp, pairs, e, used)) {
+            t.bp += used;
+#pragma unroll
+            for (int h = 0; h < 4; h++) {
+                qv[2 * h] = __byte_perm(e[h], 0u, 0x4441);
+                qv[2 * h + 1] = __byte_perm(e[h], 0u, 0x4442);
+            }
+        } else {
+            unary4<STAGED>(t.un, t.nu, t.bp, t.ok, qv);
+            unary4<STAGED>(t.un, t.nu, t.bp, t.ok, qv + 4);
+        }
         if (FORM == kFormGeneral) {
             const uint32_t gbits = group_rem_bits<N>(k, kl);
             rem_group_mixed<N, STAGED>(t.rem, t.nr, t.rb, 0, k, kl, gbits, rv);
@@ -459,14 +480,14 @@ struct AttnSmem {
     uint32_t stage[kAttnWarps][2][kAttnStage + kStagePad];
     uint32_t seg[kAttnWarps][129];
     uint32_t sign[4];
-    uint32_t pairs[1 << kPairBits];             // E8 at k = 0 (pair_entry)
+    uint32_t pairs[1 << kPairBits];             // pair_entry
     float rescale[R];                           // of the sums, this step
     float qscale[R];                            // undoes a row's power-of-two scale, with the softmax scale
     int64_t qpos[R];
     float xs[kAttnWarps][128];
     uint64_t range[3];
     int64_t span[2];                            // first and last position of the CTA's queries
-    float eref[kAttnWarps];
+    float ev[4], estep;                         // V's scales of the step's chunks (times 64), and the largest
     TopRow top[kTop];
 };
 
@@ -518,12 +539,12 @@ __device__ __forceinline__ void rotate_query(const AttnArgs &a, float (&u)[4], c
 
 // ------------------------------------------------------------------ what both kernels share
 // Chunks of a head that some query may see: [0, range[0]) and [range[1], range[2]), one bound each by the
-// first threads of warps 0 to 2 (range[0] and range[1] still to be put in order: see_bounds).
+// first threads of warps 5 to 7 (range[0] and range[1] still to be put in order: see_bounds).
 __device__ __forceinline__ void visible_range(const AttnArgs &a, const Table &tab, uint64_t *range) {
-    if (threadIdx.x == 0) range[2] = chunks_before(a, tab, a.len, true);
-    if (threadIdx.x == 32 && a.window > 0)
+    if (threadIdx.x == 160) range[2] = chunks_before(a, tab, a.len, true);
+    if (threadIdx.x == 192 && a.window > 0)
         range[0] = a.sinks > 0 ? chunks_before(a, tab, a.sinks < a.len ? a.sinks : a.len, true) : 0;
-    if (threadIdx.x == 64 && a.window > 0) {
+    if (threadIdx.x == 224 && a.window > 0) {
         const int64_t lo = (a.mask ? a.len - 1 : a.len - a.n_q) - a.window + 1;   // of any query: a bound is enough
         range[1] = lo > 0 ? chunks_before(a, tab, lo, false) : 0;
     }
@@ -724,17 +745,17 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
     // ---- which chunks the queries can see, the queries themselves
     const Table tab(a.table[0], a.n_appends, a.heads, sm.top);
     tab.load(sm.top);
-    if (threadIdx.x == 0) query_span(a, row0, R, sm.span);
+    if (threadIdx.x == 128) query_span(a, row0, R, sm.span);
     build_sign_table(sm.sign, 1, a.seed[0]);
-    if (LAT == HQ_E8 && FORM == kFormUnary)
-        for (int i = threadIdx.x; i < (1 << kPairBits); i += blockDim.x) sm.pairs[i] = pair_entry((uint32_t)i);
+    for (int i = threadIdx.x; i < (1 << kPairBits); i += blockDim.x)
+        sm.pairs[i] = pair_entry<LAT == HQ_E8 && FORM == kFormUnary>((uint32_t)i);
     for (int r = threadIdx.x; r < R; r += blockDim.x) sm.qpos[r] = query_position(a, row0 + r);
     __syncthreads();
     visible_range(a, tab, sm.range);
     __syncwarp();
     for (int r = warp; r < R; r += kAttnWarps) {
-        float u[4], up;
-        load_query(a, head, row0 + r, sm.sign, sm.xs[warp], lane, u, up);
+        float u[4] = {}, up = 1.0f;
+        if (row0 + r < a.rows) load_query(a, head, row0 + r, sm.sign, sm.xs[warp], lane, u, up);
         // fragment of coordinate c for row r: step s = (c mod 32) / 4 of lane quarter c / 32
 #pragma unroll
         for (int pr = 0; pr < 2; pr++) {
@@ -760,12 +781,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
     const uint64_t st1 = steps * (uint64_t)(split + 1) / (uint64_t)a.splits;
 
     // ---- V is summed in units of the largest scale among this CTA's appends
-    float eref = reference_scale(a, tab, ia, ib, st0 * RW, min(nvis, st1 * RW));
-    if (lane == 0) sm.eref[warp] = eref;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kAttnWarps; i++) eref = fmaxf(eref, sm.eref[i]);
-
     // softmax state of row tid / 16, the same in its 16 threads but for the sums
     float m_run = kNegInf, l_run = 0.0f, acc[2][4] = {};
 
@@ -795,9 +810,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
         else
             ok = scan_segments(gsrc + pl.nc + pl.nr, pl.nu, pl.nsym, seg, lane) && ok;
         const int r0 = RW == 4 ? 0 : wi;
-        // V in units of eref; both in units of 64
-        const float zs = which && cur.on ? __fmul_rn(__fdiv_rn(cur.e, eref), 0.015625f) : 0.015625f;
+        // codes in units of 64; the appends' scales go into the scores and, relative to the step's largest,
+        // into the weights
         const float ek = cur.on ? __fmul_rn(cur.e, 64.0f) : 0.0f;
+        if (which && r0 == 0 && lane == 0) sm.ev[ci] = ek;
         const bool open = all_see(a, cur, sm.span);
         bool bad = cur.on && !ok;
 #pragma unroll 1
@@ -809,7 +825,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
             const unsigned long long e0 = (unsigned long long)(((cur.t0 + ti) * a.heads + head) * kTile);
             // a tile that did not decode counts as zeros, as a read stores it
             const unsigned lost = decode_round<LAT, DITHER, FORM>(
-                ok, staged, st, gsrc, pl, src, seg, 32u * (uint32_t)(r0 + rr) + lane, valid, e0, zs, sm.pairs,
+                ok, staged, st, gsrc, pl, src, seg, 32u * (uint32_t)(r0 + rr) + lane, valid, e0, 0.015625f, sm.pairs,
                 [&](int g, const uint32_t (&x)[4]) {
 #pragma unroll
                     for (int i = 0; i < 4; i++) w[4 * g + i] = x[i];
@@ -871,6 +887,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
                 const float2 y = *reinterpret_cast<const float2 *>(sc);
                 x[0] = y.x; x[1] = y.y;
             }
+            float es = sm.ev[0];
+#pragma unroll
+            for (int i = 1; i < RW; i++) es = fmaxf(es, sm.ev[i]);
+            const float ratio = es > 0.0f ? __fdiv_rn(sm.ev[PT * j / 32], es) : 0.0f;
             float m = m_run;
 #pragma unroll
             for (int i = 0; i < PT; i++) m = fmaxf(m, x[i]);
@@ -880,11 +900,13 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
             const float f = ex2(__fsub_rn(m_run, base));
             m_run = m;
             if (j == 0) sm.rescale[r] = f;
+            if (threadIdx.x == 0) sm.estep = es;
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < PT; i++) {
                 x[i] = ex2(__fsub_rn(x[i], base));
                 sum = __fadd_rn(sum, x[i]);
+                x[i] = __fmul_rn(x[i], ratio);
             }
             l_run = __fmaf_rn(l_run, f, sum);
             if constexpr (PT == 8)
@@ -896,14 +918,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
         __syncthreads();   // the weights are there
         {
             // sums of this warp's 16 coordinates over the step's tokens: V^T (16 x 16) times P^T (16 x 8 rows)
-#pragma unroll
-            for (int n = 0; n < 2; n++) {
-                const float f0 = sm.rescale[8 * n + 2 * t4], f1 = sm.rescale[8 * n + 2 * t4 + 1];
-                acc[n][0] = __fmul_rn(acc[n][0], f0);
-                acc[n][1] = __fmul_rn(acc[n][1], f1);
-                acc[n][2] = __fmul_rn(acc[n][2], f0);
-                acc[n][3] = __fmul_rn(acc[n][3], f1);
-            }
+            float o[2][4] = {};
 #pragma unroll
             for (int ks = 0; ks < NT / 16; ks++) {
                 uint32_t av[4];
@@ -912,8 +927,17 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
                 uint32_t bp[4];
                 const int r = 8 * (lane >> 4) + (lane & 7), piece = 2 * ks + ((lane >> 3) & 1);
                 ldsm4(bp, sm.p + r * (NT / 2) + 4 * (RW == 4 ? piece ^ (r & 7) : piece ^ ((r >> 1) & 3)));
-                mma16816(acc[0], av, bp[0], bp[1]);
-                mma16816(acc[1], av, bp[2], bp[3]);
+                mma16816(o[0], av, bp[0], bp[1]);
+                mma16816(o[1], av, bp[2], bp[3]);
+            }
+            const float es = sm.estep;
+#pragma unroll
+            for (int n = 0; n < 2; n++) {
+                const float f0 = sm.rescale[8 * n + 2 * t4], f1 = sm.rescale[8 * n + 2 * t4 + 1];
+                acc[n][0] = __fmaf_rn(acc[n][0], f0, __fmul_rn(o[n][0], es));
+                acc[n][1] = __fmaf_rn(acc[n][1], f1, __fmul_rn(o[n][1], es));
+                acc[n][2] = __fmaf_rn(acc[n][2], f0, __fmul_rn(o[n][2], es));
+                acc[n][3] = __fmaf_rn(acc[n][3], f1, __fmul_rn(o[n][3], es));
             }
         }
         __syncthreads();   // V, the scores and the weights may be written again
@@ -924,14 +948,13 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
 
     // ---- the split's partial results
     const int64_t pbase = ((int64_t)split * a.heads + head) * a.row_pad + row0;
-    const float eo = __fmul_rn(eref, 64.0f);
 #pragma unroll
     for (int n = 0; n < 2; n++) {
         float *o = a.part + (pbase + 8 * n + 2 * t4) * kTile + 16 * warp + g8;
-        o[0] = __fmul_rn(acc[n][0], eo);
-        o[kTile] = __fmul_rn(acc[n][1], eo);
-        o[8] = __fmul_rn(acc[n][2], eo);
-        o[kTile + 8] = __fmul_rn(acc[n][3], eo);
+        o[0] = acc[n][0];
+        o[kTile] = acc[n][1];
+        o[8] = acc[n][2];
+        o[kTile + 8] = acc[n][3];
     }
     {
         float l = l_run;
@@ -1068,8 +1091,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
     const Table tab(a.table[0], a.n_appends, a.heads, sm.top);
     tab.load(sm.top);
     build_sign_table(sm.sign, 1, a.seed[0]);
-    if (LAT == HQ_E8 && FORM == kFormUnary)
-        for (int i = threadIdx.x; i < (1 << kPairBits); i += blockDim.x) sm.pairs[i] = pair_entry((uint32_t)i);
+    for (int i = threadIdx.x; i < (1 << kPairBits); i += blockDim.x)
+        sm.pairs[i] = pair_entry<LAT == HQ_E8 && FORM == kFormUnary>((uint32_t)i);
     for (int r = threadIdx.x; r < kWideRows; r += blockDim.x) sm.qpos[r] = query_position(a, row0 + r);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
