@@ -435,28 +435,34 @@ __device__ __forceinline__ void decode_block(Quarter &t, int k, int kl, uint64_t
 __device__ __forceinline__ bool close_quarter(const Quarter &t) { return t.ok && t.bp <= t.nu * 32u; }
 
 // ------------------------------------------------------------------ segment starts
-// Where each 32-symbol segment of a chunk starts: seg[s] = 32 i + n says that terminator 32 s - 1 is
-// the n-th (0-based) set bit of unary word i.  32 words at a time, a lane to a word: population
-// counts, a scan of two sets packed in one register, and every word that holds a boundary (at most
-// one) notes it; each lane finds the bit itself for the segments it decodes (segment_start).  False
+// Where the 32-symbol segments [s0, s1) of a chunk start (s1 - s0 = 32 rounds' worth of what the warp
+// decodes): seg[s] = 32 i + n says that terminator 32 s - 1 is the n-th (0-based) set bit of unary word i.
+// 64 words at a time, a lane to two words: population counts, a scan of both packed in one register, and
+// every word that holds a boundary (at most one) notes it; each lane finds the bit itself for the segments
+// it decodes (segment_start).  Words wholly before or behind the wanted segments are only counted.  False
 // unless the plane holds exactly nsym terminators.
-__device__ __forceinline__ bool scan_segments(const uint32_t *un, uint32_t nu, uint32_t nsym, uint32_t *seg, int lane) {
+__device__ __forceinline__ bool scan_segments(const uint32_t *un, uint32_t nu, uint32_t nsym, uint32_t s0, uint32_t s1,
+                                              uint32_t *seg, int lane) {
     uint32_t seen = 0;
+    const uint32_t want0 = 32u * s0, want1 = 32u * s1;   // terminators want0 - 1 .. want1 - 33 are looked for
     for (uint32_t i0 = 0; i0 < nu; i0 += 64) {
         const uint32_t i = i0 + lane;
         const uint32_t p0 = i < nu ? __popc(un[i]) : 0u, p1 = i + 32u < nu ? __popc(un[i + 32u]) : 0u;
-        uint32_t both = p0 | p1 << 16;
+        const uint32_t total = __reduce_add_sync(0xffffffffu, p0 + p1);
+        if (seen + total >= want0 && seen < want1) {
+            uint32_t both = p0 | p1 << 16;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, both, o);
-            if (lane >= o) both += v;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, both, o);
+                if (lane >= o) both += v;
+            }
+            const uint32_t all = __shfl_sync(0xffffffffu, both, 31);
+            const uint32_t b0 = seen + (both & 0xFFFFu) - p0, b1 = seen + (all & 0xFFFFu) + (both >> 16) - p1;
+            // a boundary past the last segment means a corrupt plane: not noted, and found by the count
+            if ((b0 >> 5) != ((b0 + p0) >> 5) && b0 < nsym) seg[(b0 >> 5) + 1u] = i * 32u + (31u - (b0 & 31u));
+            if ((b1 >> 5) != ((b1 + p1) >> 5) && b1 < nsym) seg[(b1 >> 5) + 1u] = (i + 32u) * 32u + (31u - (b1 & 31u));
         }
-        const uint32_t all = __shfl_sync(0xffffffffu, both, 31);
-        const uint32_t b0 = seen + (both & 0xFFFFu) - p0, b1 = seen + (all & 0xFFFFu) + (both >> 16) - p1;
-        // a boundary past the last segment means a corrupt plane: not noted, and found by the count
-        if ((b0 >> 5) != ((b0 + p0) >> 5) && b0 < nsym) seg[(b0 >> 5) + 1u] = i * 32u + (31u - (b0 & 31u));
-        if ((b1 >> 5) != ((b1 + p1) >> 5) && b1 < nsym) seg[(b1 >> 5) + 1u] = (i + 32u) * 32u + (31u - (b1 & 31u));
-        seen += (all & 0xFFFFu) + (all >> 16);
+        seen += total;
     }
     __syncwarp();
     return seen == nsym;
@@ -613,6 +619,8 @@ struct Source {
     uint64_t cap, seed;
     int which, k, kl;
     AttnRow row;
+    bool same;    // V: its append covers the same tokens as K's
+    float e;      // the append's scale in this cache
     __device__ __forceinline__ void init(const AttnArgs &a, int w) {
         which = w;
         words = a.words[w];
@@ -635,21 +643,24 @@ struct Source {
         p.w0 = p.w1 = 0;
         if (p.on) {
             const uint64_t i = v < ia ? v : v - ia + ib;
-            find_row(a, tab, i, row);
+            if (!(i >= row.base && i < row.base + row.count)) {
+                find_row(a, tab, i, row);
+                same = true;
+                e = row.row.scale_inv;
+                if (which) {
+                    const hq_kv_append_row vr = a.table[1][row.append];
+                    same = vr.first_chunk == row.row.first_chunk && vr.token0 == row.row.token0 &&
+                           vr.tokens == row.row.tokens;
+                    e = vr.scale_inv;
+                }
+            }
             const uint64_t j = i - row.base;
             p.t0 = row.row.token0 + 32 * (int64_t)j;
             const int64_t left = (int64_t)row.row.tokens - 32 * (int64_t)j;
             p.n = (int)(left < 32 ? left : 32);
             const uint64_t chunk = row.row.first_chunk + (uint64_t)head * row.count + j;
-            p.e = row.row.scale_inv;
-            p.ok = chunk < a.n_chunks;
-            if (which) {
-                // V's append has to cover the same tokens
-                const hq_kv_append_row vr = a.table[1][row.append];
-                p.ok = p.ok && vr.first_chunk == row.row.first_chunk && vr.token0 == row.row.token0 &&
-                       vr.tokens == row.row.tokens;
-                p.e = vr.scale_inv;
-            }
+            p.e = e;
+            p.ok = same && chunk < a.n_chunks;
             if (p.ok) {
                 p.w0 = offsets[chunk];
                 p.w1 = offsets[chunk + 1];
@@ -702,7 +713,7 @@ __device__ __forceinline__ unsigned decode_round(const uint32_t *p, const Planes
                                                  uint32_t segi, bool valid, unsigned long long e0, float scale,
                                                  const uint32_t *pairs, F &&use) {
     if (!valid) {
-        segi &= 3u;
+        segi = 0u;   // its start needs no note
         scale = 0.0f;
     }
     Quarter t;
@@ -805,10 +816,11 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
         const uint32_t *const st = sm.stage[warp][buf], *const gsrc = src.words + cur.w0;
         uint32_t *const seg = sm.seg[warp];
         bool ok = pl.ok;
+        const uint32_t seg0 = RW == 4 ? 0u : 32u * wi, seg1 = RW == 4 ? 128u : seg0 + 32u;
         if (staged)
-            ok = scan_segments(st + pl.nc + pl.nr, pl.nu, pl.nsym, seg, lane) && ok;
+            ok = scan_segments(st + pl.nc + pl.nr, pl.nu, pl.nsym, seg0, seg1, seg, lane) && ok;
         else
-            ok = scan_segments(gsrc + pl.nc + pl.nr, pl.nu, pl.nsym, seg, lane) && ok;
+            ok = scan_segments(gsrc + pl.nc + pl.nr, pl.nu, pl.nsym, seg0, seg1, seg, lane) && ok;
         const int r0 = RW == 4 ? 0 : wi;
         // codes in units of 64; the appends' scales go into the scores and, relative to the step's largest,
         // into the weights
@@ -1163,10 +1175,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
         const uint32_t *const st = sm.stage[chunk_slot][buf], *const gsrc = src.words + cur.w0;
         uint32_t *const seg = sm.seg[warp];
         bool ok = pl.ok;
+        const uint32_t seg0 = 32u * r0, seg1 = seg0 + 64u;
         if (staged)
-            ok = scan_segments(st + pl.nc + pl.nr, pl.nu, pl.nsym, seg, lane) && ok;
+            ok = scan_segments(st + pl.nc + pl.nr, pl.nu, pl.nsym, seg0, seg1, seg, lane) && ok;
         else
-            ok = scan_segments(gsrc + pl.nc + pl.nr, pl.nu, pl.nsym, seg, lane) && ok;
+            ok = scan_segments(gsrc + pl.nc + pl.nr, pl.nu, pl.nsym, seg0, seg1, seg, lane) && ok;
         if (which == 0 && r0 == 0 && lane == 0) {
             WideInfo &w = sm.info[ci];
             w.t0 = cur.t0;
