@@ -1115,9 +1115,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
     __syncwarp();
 
     // ---- queries: upper parts to their tiles, lower parts through the K and V tiles to TMEM
+#pragma unroll 4
     for (int r = warp; r < 128 * nb; r += 16) {
-        float u[4], up;
-        load_query(a, head, row0 + r, sm.sign, reinterpret_cast<float *>(sm.seg[warp]), lane, u, up);
+        float u[4] = {}, up = 1.0f;
+        if (r < rows) load_query(a, head, row0 + r, sm.sign, reinterpret_cast<float *>(sm.seg[warp]), lane, u, up);
         const uint32_t h0 = h2_pack(u[0], u[1]), h1 = h2_pack(u[2], u[3]);
         const __half2 a0 = *reinterpret_cast<const __half2 *>(&h0), a1 = *reinterpret_cast<const __half2 *>(&h1);
         const uint32_t l0 = h2_pack(__fsub_rn(u[0], __low2float(a0)), __fsub_rn(u[1], __high2float(a0)));

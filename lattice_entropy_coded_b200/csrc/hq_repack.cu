@@ -135,7 +135,7 @@ __device__ __forceinline__ bool tile_starts(const uint32_t *un, uint32_t nu, uin
     return true;
 }
 
-__global__ void __launch_bounds__(kRepackWarps * 32) repack_measure(const __grid_constant__ RepackArgs a) {
+__global__ void __launch_bounds__(kRepackWarps * 32, 12) repack_measure(const __grid_constant__ RepackArgs a) {
     __shared__ uint32_t starts[kRepackWarps][36];
     __shared__ TopRow top[kTop];
     __shared__ uint32_t size_of[kRepackWarps];
@@ -366,7 +366,7 @@ __device__ __forceinline__ void copy_plane(const RepackArgs &a, uint32_t *dst, u
     }
 }
 
-__global__ void __launch_bounds__(kRepackWarps * 32) repack_copy(const __grid_constant__ RepackArgs a) {
+__global__ void __launch_bounds__(kRepackWarps * 32, 12) repack_copy(const __grid_constant__ RepackArgs a) {
     __shared__ unsigned long long tmp[kRepackWarps];
     __shared__ unsigned long long from[kRepackWarps][3][32];   // first source bit of each run, by plane
     __shared__ uint32_t at[kRepackWarps][3][34];               // and its first bit in the new plane
@@ -569,8 +569,8 @@ extern "C" int hq_kv_repack(const hq_kv_cache *src, hq_kv_cache *dst, const int6
     const uint64_t ctas = (a.n_chunks + kRepackWarps - 1) / kRepackWarps;
     repack_measure<<<(unsigned)ctas, kRepackWarps * 32, 0, s>>>(a);
     if (cudaGetLastError() != cudaSuccess) return HQ_ECUDA;
-    // all resident at once (16 CTAs of 128 threads per SM): each sums the sizes before its own chunks
-    const uint64_t most = 148 * 16;
+    // all resident at once (12 CTAs per SM): each sums the sizes before its own chunks
+    const uint64_t most = 148 * 12;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(ctas < most ? ctas : most));
     cfg.blockDim = dim3(kRepackWarps * 32);
