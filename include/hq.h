@@ -458,7 +458,7 @@ typedef struct hq_attn_spec {
 } hq_attn_spec;     /* 40 bytes */
 
 /* Device workspace of hq_kv_attention and hq_kv_tree_attention for caches of `heads` KV heads
- * of any length (partial results of the splits of the tokens: at most about 16 MB for 8 heads).
+ * of any length (partial results of the splits of the tokens: at most about 20 MB for 8 heads).
  * Host only. */
 HQ_API int hq_kv_attention_workspace_bytes(int32_t heads, const hq_attn_spec *spec, size_t *bytes);
 
@@ -476,7 +476,9 @@ HQ_API int hq_kv_attention_workspace_bytes(int32_t heads, const hq_attn_spec *sp
  *               the visible tokens (-infinity if none), to merge with attention over others.
  *   workspace : >= hq_kv_attention_workspace_bytes, 16-byte aligned; its contents need no
  *               initialisation; two calls that may run at once need one each.
- * A corrupt chunk's tokens count as zero vectors, and HQ_ST_CORRUPT goes to its cache's d_stats.
+ * A corrupt chunk's tokens count as zero vectors, and HQ_ST_CORRUPT goes to its cache's d_stats
+ * (HQ_ST_TIMEOUT: the tensor cores did not answer; the output is unspecified).  The same inputs
+ * give the same bits.
  * n_q 0 does nothing.  Asynchronous on cuda_stream; the counters and the spec are those at the
  * call (or its capture). */
 HQ_API int hq_kv_attention(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *spec, const void *d_q,

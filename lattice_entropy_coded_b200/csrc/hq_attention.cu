@@ -311,7 +311,7 @@ int attend(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *sp, c
         if (a.window > 0) {
             const uint64_t w = (uint64_t)(a.window + sp->n_q + a.sinks) + 4;
             // at the cache's average of tokens to a chunk (only the split depends on it)
-            const uint64_t c = w * per_head / (uint64_t)(k->tokens > 0 ? k->tokens : 1) + 2;
+            const uint64_t c = (uint64_t)((double)w * (double)per_head / (double)k->tokens) + 2;
             if (c < per_head) per_head = c;
         }
         a.splits = attn_splits(a.heads, a.rows, per_head);

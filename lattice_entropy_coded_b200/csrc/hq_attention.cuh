@@ -7,21 +7,23 @@
 // rotated once, the output once, and no token's tile is transformed.  The softmax runs over
 // the tokens as they come, with the running maximum and sum of each row.
 //
-// Two launches: attention_kernel, a grid of (splits of the tokens) x (KV heads) x (blocks of
-// query rows), leaves a partial (maximum, sum, 128 sums of values) per row and split, in the
-// rotated domain; attention_combine joins the splits, turns the result back, adds the drafted
-// tokens of a tree (whose K and V are plain bf16) and writes the output.
+// Two launches: attention_kernel (up to 16 query rows of a KV head) or attention_wide (up to 256), a grid
+// of (splits of the tokens) x (KV heads) x (blocks of rows), leaves a partial (maximum, sum, 128 sums of
+// values) per row and split, in the rotated domain; attention_combine joins the splits, turns the result
+// back, adds the drafted tokens of a tree (whose K and V are plain bf16) and writes the output.
 //
-// The products run on the tensor cores in fp16 with fp32 sums (mma.sync m16n8k16):
+// The products run on the tensor cores in fp16 with fp32 sums:
 //  * z / 64 in fp16: exact for codes up to 2048 without dither, else rounded by at most 2^-11
 //    of its value, and finite over the codec's whole range (|z| < 2^21 + 2 < 64 * 65504);
 //  * the rotated queries as the sum of two fp16 (scaled by a power of two per row): 2^-22;
-//  * the weights p in [0, 1] in fp16: 2^-11 of their value (2^-25 below 2^-14).
-// A lane of the Rice decoder holds 32 consecutive coordinates of one token; a step of 16
-// contracted coordinates takes 4 from each of the 4 lanes of a token, and the queries are laid
-// out in the same order, so K goes from the decoder's registers into the product as it is.
+//  * the weights p in fp16: 2^-11 of their value (2^-25 of the row's largest below 2^-14).
+// In attention_kernel a lane of the Rice decoder holds 32 consecutive coordinates of one token; a step of
+// 16 contracted coordinates (mma.sync m16n8k16) takes 4 from each of the 4 lanes of a token, and the queries
+// are laid out in the same order, so K goes from the decoder's registers into the product as it is.
 //
-// Bound: the decoder's integer work (see hq_decode.cuh), not bytes nor products.
+// Bound: the decoder's integer work, not bytes nor products: 38 lane-instructions a code with dither (E8, 2
+// bits), at 3.4 of 4 issued a cycle. One query over 8 x 32768 tokens at 2 bits: 177 us (104 of them the
+// decode's at that rate); 64 drafts: 300 us.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -351,3 +351,62 @@ def test_dither_of_many_blocks(k):
         out = at(q, torch.empty(1, heads, 128, device="cuda"), length=t + 1)
         err = (out[0].double() - v[:, t]).norm(dim=-1)
         assert bool((err <= 2.0 ** -10 * v[:, t].norm(dim=-1)).all())
+
+
+@pytest.mark.parametrize("ones", [127, 128, 129, 300])
+def test_more_appends_than_the_table_sample(ones):
+    """The append table is searched through a sample of 128 appends; a token an append, and longer ones between."""
+    a, b = T.pair(2, [40] + [1] * ones + [33, 1, 70], "E8")
+    _run(a, b, 2, n_q=2)
+    _run(a, b, 16, n_q=2)                                   # many rows
+    _run(a, b, 2, n_q=3, window=90, sinks=41)
+    _run(a, b, 2, length=40 + ones // 2, window=20, sinks=3)
+
+
+def test_scales_far_apart_among_many_rows():
+    """Appends whose alphas differ by 2^12: the rarest scale must not swamp the others."""
+    a, b = T.pair(1, [32, 32, 40, 1, 1], "E8", 0, 0, alphas=[1.0, 1.0, 4.0, 0.5, 2.0])
+    _run(a, b, 3, dither=0)
+    _run(a, b, 32, n_q=2, dither=0)
+
+
+def test_dense_rotation_of_many_rows():
+    hq = _hq()
+    rot = [hq.hq_haar_rotation(5), hq.hq_haar_rotation(6)]
+    torch.cuda.synchronize()
+    a, b = T.pair(2, [100, 1, 30], "E8", 1, alpha=0.7, rotation=rot)
+    _run(a, b, 12, n_q=12)
+    _tree(a, b, 8, [-1, 0, 0, 2, 3, 3, 3])
+
+
+def test_many_rows_bf16_strides_and_bad_rows():
+    """attention of 130 rows a head (two blocks, the second of two rows): NaN and infinity stay in their rows, a
+    corrupt chunk counts as zeros, what lies between the output's rows stays."""
+    hq = _hq()
+    a, b = T.pair(2, [256, 20], "D4")
+    q = _queries(26, 10)
+    buf = torch.full((26, 10, 136), 7.0, device="cuda")
+    out = buf[:, :, :128]
+    at = hq.KVAttention(a, b, 5)
+    at(q, out)
+    T.check(out, None, q, T.vectors(a), T.vectors(b), T.seen(26, 276, 0, 0), 5, SCALE, 1)
+    assert bool((buf[:, :, 128:] == 7).all())
+    want = out.clone()
+    q[3, 1, 5], q[25, 9, 0] = float("nan"), float("inf")
+    at(q, out)
+    rows = torch.ones(26, 10, dtype=torch.bool, device="cuda")
+    rows[3, 1] = rows[25, 9] = False
+    assert torch.equal(out[rows], want[rows]) and not torch.isfinite(out[~rows]).any()
+    q[3, 1, 5], q[25, 9, 0] = 0, 0
+    keep = b.offsets.clone()
+    b.offsets[2], b.offsets[3] = keep[3], keep[2]
+    at(q, out)
+    assert hq.read_stats(b.stats)["status"] == hq.HQ_ST_CORRUPT and hq.read_stats(a.stats)["status"] == 0
+    T.check(out, None, q, T.vectors(a), T.vectors(b), T.seen(26, 276, 0, 0), 5, SCALE, 1)
+
+
+def test_rows_of_many_heads_and_blocks():
+    """More rows than a CTA takes (64 queries x 9 heads a KV head: three blocks of rows)."""
+    a, b = T.pair(2, [300], "Z", 1)
+    _run(a, b, 9, n_q=64)
+    _run(a, b, 9, n_q=64, window=40, sinks=2, length=290)

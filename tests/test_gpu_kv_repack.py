@@ -98,6 +98,9 @@ def test_every_stream_form(lat, k, dk, dither):
     ([4, 3, 2, 1, 5] * 7, [(0, 105)]),
     ([256, 256, 17], [(0, 4), (300, 529)]),
     ([700], [(i * 21, i * 21 + 20) for i in range(32)]),
+    ([1] * 300 + [64], [(0, 1), (7, 331), (340, 364)]),
+    ([17] * 20, [(0, 340)]),
+    ([96, 31, 64], [(0, 96), (96, 191)]),
 ])
 @pytest.mark.parametrize("heads", [1, 3])
 def test_cuts(appends, ranges, heads):

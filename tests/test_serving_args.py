@@ -12,6 +12,12 @@ def _hq():
     return hq
 
 
+def test_struct_layouts_match_header():
+    hq = _hq()
+    assert C.sizeof(hq.hq_attn_spec) == 40 and hq.hq_attn_spec.scale.offset == 24 and hq.hq_attn_spec.group.offset == 32
+    assert C.sizeof(hq.hq_rope_spec) == 16 and hq.hq_rope_spec.eps.offset == 12
+
+
 def _cache(at, heads=2, tokens=100, chunks=8, appends=1, **kw):
     hq = _hq()
     p = dict(lattice="E8", alpha=1.0, rice_k=1, seed=at, dither=1)
