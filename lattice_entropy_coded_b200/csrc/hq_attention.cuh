@@ -793,7 +793,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
     const uint64_t st0 = steps * (uint64_t)split / (uint64_t)a.splits;
     const uint64_t st1 = steps * (uint64_t)(split + 1) / (uint64_t)a.splits;
 
-    // ---- V is summed in units of the largest scale among this CTA's appends
     // softmax state of row tid / 16, the same in its 16 threads but for the sums
     float m_run = kNegInf, l_run = 0.0f, acc[2][4] = {};
 
