@@ -95,6 +95,7 @@ inline int attn_splits(int heads, int rows, uint64_t chunks_per_head) {
 
 namespace {
 
+constexpr int kTop = 128;   // rows of the append table sampled into shared memory
 constexpr float kNegInf = -INFINITY;
 
 __device__ __forceinline__ uint32_t h2_pack(float a, float b) {
@@ -138,12 +139,12 @@ __device__ __forceinline__ void load_row(const AttnArgs &a, uint64_t append, Att
     r.base = base;
     r.count = (uint64_t)(((int64_t)r.row.tokens + 31) / 32);
 }
-__device__ __forceinline__ void find_row(const AttnArgs &a, const Table &t, uint64_t i, AttnRow &r) {
+__device__ __forceinline__ void find_row(const AttnArgs &a, const Table<kTop> &t, uint64_t i, AttnRow &r) {
     if (i >= r.base && i < r.base + r.count) return;
     load_row(a, t.append_of(i), r);
 }
 // Per-head chunks that lie wholly before token t (round_up: that hold any token before t).
-__device__ __forceinline__ uint64_t chunks_before(const AttnArgs &a, const Table &tab, int64_t t, bool round_up) {
+__device__ __forceinline__ uint64_t chunks_before(const AttnArgs &a, const Table<kTop> &tab, int64_t t, bool round_up) {
     AttnRow r;
     load_row(a, tab.append_of_token(t), r);
     const int64_t in = t - r.row.token0;
@@ -548,7 +549,7 @@ __device__ __forceinline__ void rotate_query(const AttnArgs &a, float (&u)[4], c
 // ------------------------------------------------------------------ what both kernels share
 // Chunks of a head that some query may see: [0, range[0]) and [range[1], range[2]), one bound each by the
 // first threads of warps 5 to 7 (range[0] and range[1] still to be put in order: see_bounds).
-__device__ __forceinline__ void visible_range(const AttnArgs &a, const Table &tab, uint64_t *range) {
+__device__ __forceinline__ void visible_range(const AttnArgs &a, const Table<kTop> &tab, uint64_t *range) {
     if (threadIdx.x == 160) range[2] = chunks_before(a, tab, a.len, true);
     if (threadIdx.x == 192 && a.window > 0)
         range[0] = a.sinks > 0 ? chunks_before(a, tab, a.sinks < a.len ? a.sinks : a.len, true) : 0;
@@ -604,7 +605,7 @@ __device__ __forceinline__ void load_query(const AttnArgs &a, int head, int row,
 }
 // The largest of V's scales among the appends of visible chunks [v0, v1), over a warp (each warp takes its
 // share of the appends; the caller joins them): V is summed in its units.
-__device__ __forceinline__ float reference_scale(const AttnArgs &a, const Table &tab, uint64_t ia, uint64_t ib, uint64_t v0, uint64_t v1) {
+__device__ __forceinline__ float reference_scale(const AttnArgs &a, const Table<kTop> &tab, uint64_t ia, uint64_t ib, uint64_t v0, uint64_t v1) {
     float e = 0.0f;
     if (v0 >= v1) return e;
     const uint64_t lo = tab.append_of(v0 < ia ? v0 : v0 - ia + ib), hi = tab.append_of(v1 - 1 < ia ? v1 - 1 : v1 - 1 - ia + ib);
@@ -634,7 +635,7 @@ struct Source {
         row.base = row.count = 0;   // none yet
     }
     // visible chunk v
-    __device__ __forceinline__ Piece piece(const AttnArgs &a, const Table &tab, int head, uint64_t v, bool on, uint64_t nvis, uint64_t ia,
+    __device__ __forceinline__ Piece piece(const AttnArgs &a, const Table<kTop> &tab, int head, uint64_t v, bool on, uint64_t nvis, uint64_t ia,
                                            uint64_t ib) {
         Piece p;
         p.on = on && v < nvis;
@@ -756,7 +757,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
 
     cudaTriggerProgrammaticLaunchCompletion();   // the combine may come up; it waits for this grid's end
     // ---- which chunks the queries can see, the queries themselves
-    const Table tab(a.table[0], a.n_appends, a.heads, sm.top);
+    const Table<kTop> tab(a.table[0], a.n_appends, a.heads, sm.top);
     tab.load(sm.top);
     if (threadIdx.x == 128) query_span(a, row0, R, sm.span);
     build_sign_table(sm.sign, 1, a.seed[0]);
@@ -1101,7 +1102,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    const Table tab(a.table[0], a.n_appends, a.heads, sm.top);
+    const Table<kTop> tab(a.table[0], a.n_appends, a.heads, sm.top);
     tab.load(sm.top);
     build_sign_table(sm.sign, 1, a.seed[0]);
     for (int i = threadIdx.x; i < (1 << kPairBits); i += blockDim.x)

@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kMaxRanges = 32;
 constexpr int kRepackWarps = 4;
+constexpr int kTop = 512;   // rows of the append table sampled into shared memory
 
 struct RepackRange {
     int64_t begin, end;
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kRepackWarps * 32, 12) repack_measure(const __
     __shared__ uint32_t size_of[kRepackWarps];
     cudaTriggerProgrammaticLaunchCompletion();   // the second launch may come up; it waits for this grid's end
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Table tab(a.src_table, a.src_appends, a.heads, top);
+    const Table<kTop> tab(a.src_table, a.src_appends, a.heads, top);
     tab.load(top);
     __syncthreads();
     if (blockIdx.x == 0) {

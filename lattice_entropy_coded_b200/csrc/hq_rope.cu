@@ -13,8 +13,9 @@
 // 4 pairs, so the rotation needs no exchange and the norm four shuffles.  A half-warp keeps
 // its token's 4 angles and the side's 8 weights and walks over heads, so the sines cost one
 // evaluation per token and lane; short calls spread a token's heads over more half-warps instead.
-// 8191 tokens of 32 + 8 heads: 41 us, 4.1 TB/s (63 % of a copy); four CTAs to an SM at 64 registers (three:
-// 51 us, five: 62 us, by events on a cold L2 against 47).
+// 8191 tokens of 32 + 8 heads: 34 us, 4.9 TB/s (75 % of a copy).  Four CTAs to an SM at 64 registers (by events on
+// a cold L2: three 51 us, four 47, five 62); 8 pairs to a lane instead of 4 60 us, the next heads' loads ahead of
+// this one's arithmetic 47 to 68 us, the fast sines no difference.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -276,10 +277,11 @@ extern "C" int hq_qk_norm_rope(const void *q, int64_t q_ld_token, int64_t q_ld_h
     a.interleaved = spec->interleaved;
     a.norm = spec->norm;
     a.eps = spec->eps;
-    // a token's heads over as many half-warps as keep the GPU's (148 SMs x 2048 threads) busy, one to
-    // kRopeUnroll heads each at the least
+    // a token's heads over as many half-warps as the GPU holds (148 SMs x 4 CTAs x 256 threads), one head each
+    // at the least: every half-warp starts with its token's position and sines, so no more (8191 tokens, cold
+    // L2: 47 us with twice as many, 39 so)
     const int heads = heads_q + heads_k;
-    const int64_t want = (INT64_C(148) * 128) / tokens;
+    const int64_t want = (INT64_C(148) * 64) / tokens;
     int64_t splits = want < 1 ? 1 : want;
     if (splits > heads) splits = heads;
     a.per_split = (int)((heads + splits - 1) / splits);

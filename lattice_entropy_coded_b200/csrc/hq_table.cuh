@@ -7,21 +7,21 @@
 
 namespace hq {
 
-// The append table is searched through a sample of it in shared memory (all of it up to kTop appends):
+// The append table is searched through a sample of it in shared memory (all of it up to TOP appends):
 // one load's latency for the sample instead of one for every step of a search, which on a short cache
 // was most of a kernel's time.
-constexpr int kTop = 128;
 struct TopRow {
     uint64_t first_chunk;
     int64_t token0;
 };
+template <int TOP>
 struct Table {
     const hq_kv_append_row *rows;
     const TopRow *top;
     uint64_t n_appends, heads, stride, n;   // sample s is append s * stride
     __device__ __forceinline__ Table(const hq_kv_append_row *table, uint64_t appends, int h, const TopRow *t)
         : rows(table), top(t), n_appends(appends), heads((uint64_t)h) {
-        stride = (n_appends + kTop - 1) / kTop;
+        stride = (n_appends + TOP - 1) / TOP;
         n = (n_appends + stride - 1) / stride;
     }
     // by the whole CTA; the caller synchronises
