@@ -440,7 +440,7 @@ __device__ __forceinline__ bool close_quarter(const Quarter &t) { return t.ok &&
 // ------------------------------------------------------------------ segment starts
 // Where the 32-symbol segments [s0, s1) of a chunk start (s1 - s0 = 32 rounds' worth of what the warp
 // decodes): seg[s] = 32 i + n says that terminator 32 s - 1 is the n-th (0-based) set bit of unary word i.
-// 64 words at a time, a lane to two words: population counts, a scan of both packed in one register, and
+// 128 words at a time, a lane to four words: population counts, a scan of two packed in one register, and
 // every word that holds a boundary (at most one) notes it; each lane finds the bit itself for the segments
 // it decodes (segment_start).  Words wholly before or behind the wanted segments are only counted.  False
 // unless the plane holds exactly nsym terminators.
@@ -448,22 +448,33 @@ __device__ __forceinline__ bool scan_segments(const uint32_t *un, uint32_t nu, u
                                               uint32_t *seg, int lane) {
     uint32_t seen = 0;
     const uint32_t want0 = 32u * s0, want1 = 32u * s1;   // terminators want0 - 1 .. want1 - 33 are looked for
-    for (uint32_t i0 = 0; i0 < nu; i0 += 64) {
-        const uint32_t i = i0 + lane;
-        const uint32_t p0 = i < nu ? __popc(un[i]) : 0u, p1 = i + 32u < nu ? __popc(un[i + 32u]) : 0u;
-        const uint32_t total = __reduce_add_sync(0xffffffffu, p0 + p1);
+    for (uint32_t i0 = 0; i0 < nu; i0 += 128) {
+        uint32_t p[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++) p[u] = i0 + 32u * u + lane < nu ? __popc(un[i0 + 32u * u + lane]) : 0u;
+        const uint32_t total = __reduce_add_sync(0xffffffffu, (p[0] + p[1]) + (p[2] + p[3]));
         if (seen + total >= want0 && seen < want1) {
-            uint32_t both = p0 | p1 << 16;
+            uint32_t both[2] = {p[0] | p[1] << 16, p[2] | p[3] << 16};
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, both, o);
-                if (lane >= o) both += v;
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const uint32_t v = __shfl_up_sync(0xffffffffu, both[h], o);
+                    if (lane >= o) both[h] += v;
+                }
             }
-            const uint32_t all = __shfl_sync(0xffffffffu, both, 31);
-            const uint32_t b0 = seen + (both & 0xFFFFu) - p0, b1 = seen + (all & 0xFFFFu) + (both >> 16) - p1;
-            // a boundary past the last segment means a corrupt plane: not noted, and found by the count
-            if ((b0 >> 5) != ((b0 + p0) >> 5) && b0 < nsym) seg[(b0 >> 5) + 1u] = i * 32u + (31u - (b0 & 31u));
-            if ((b1 >> 5) != ((b1 + p1) >> 5) && b1 < nsym) seg[(b1 >> 5) + 1u] = (i + 32u) * 32u + (31u - (b1 & 31u));
+            uint32_t before = seen;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint32_t all = __shfl_sync(0xffffffffu, both[h], 31), i = i0 + 64u * h + lane;
+                const uint32_t b0 = before + (both[h] & 0xFFFFu) - p[2 * h];
+                const uint32_t b1 = before + (all & 0xFFFFu) + (both[h] >> 16) - p[2 * h + 1];
+                // a boundary past the last segment means a corrupt plane: not noted, and found by the count
+                if ((b0 >> 5) != ((b0 + p[2 * h]) >> 5) && b0 < nsym) seg[(b0 >> 5) + 1u] = i * 32u + (31u - (b0 & 31u));
+                if ((b1 >> 5) != ((b1 + p[2 * h + 1]) >> 5) && b1 < nsym)
+                    seg[(b1 >> 5) + 1u] = (i + 32u) * 32u + (31u - (b1 & 31u));
+                before += (all & 0xFFFFu) + (all >> 16);
+            }
         }
         seen += total;
     }
