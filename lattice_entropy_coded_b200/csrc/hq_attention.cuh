@@ -820,7 +820,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
     for (uint64_t step = st0; step < st1; step++, buf ^= 1) {
         // the next chunk's words behind this one's decode, and the offsets of the one after it
         src.stage(next, sm.stage[warp][buf ^ 1], lane, 32);
-        const Piece after = src.piece(a, tab, head, (step + 2) * RW + ci, step + 2 < st1, nvis, ia, ib);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
         Planes pl;
@@ -897,6 +896,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
             }
         }
         if (bad) status |= HQ_ST_CORRUPT;
+        const Piece after = src.piece(a, tab, head, (step + 2) * RW + ci, step + 2 < st1, nvis, ia, ib);
         __syncthreads();   // scores and V are there
         {
             // softmax: 16 threads to a row, NT / 16 tokens each
@@ -1179,7 +1179,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
     Piece next = src.piece(a, tab, head, (st0 + 1) * 4 + ci, st0 + 1 < st1, nvis, ia, ib);
     for (uint64_t step = st0; step < st1; step++, buf ^= 1) {
         src.stage(next, sm.stage[chunk_slot][buf ^ 1], threadIdx.x & 63, 64);
-        const Piece after = src.piece(a, tab, head, (step + 2) * 4 + ci, step + 2 < st1, nvis, ia, ib);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         // the chunk's words come from both of its warps
         asm volatile("bar.sync %0, 64;" ::"r"(1 + chunk_slot) : "memory");
@@ -1227,6 +1226,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
             }
         }
         if (bad) status |= HQ_ST_CORRUPT;
+        // (found here, not before the decode: it would take registers from it)
+        const Piece after = src.piece(a, tab, head, (step + 2) * 4 + ci, step + 2 < st1, nvis, ia, ib);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         dead = __syncthreads_or(dead);   // K, V and the chunks' records are there
