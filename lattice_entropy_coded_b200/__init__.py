@@ -613,11 +613,13 @@ class KVCache:
         """dst's contents become the tokens of `ranges` of this cache (default: all of them, one range), in
         full chunks; dst: another KVCache of the same heads and params."""
         ranges = ([(0, self.tokens)] if self.tokens else []) if ranges is None else ranges
-        ws = torch.empty(hq_kv_repack_workspace_bytes(self.heads, ranges), dtype=torch.uint8, device=dst.words.device)
+        need = hq_kv_repack_workspace_bytes(self.heads, ranges)
+        # a workspace of the stream that uses it: its memory is free there before the call and after it
+        stream = cuda_stream if cuda_stream is None or isinstance(cuda_stream, torch.cuda.Stream) else \
+            torch.cuda.ExternalStream(int(cuda_stream))
+        with torch.cuda.stream(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device=dst.words.device)
         hq_kv_repack(self.cache, dst.cache, ranges, ws, cuda_stream)
-        if cuda_stream is not None:   # torch may reuse the workspace's memory only after that stream is done with it
-            ws.record_stream(cuda_stream if isinstance(cuda_stream, torch.cuda.Stream)
-                             else torch.cuda.ExternalStream(int(cuda_stream)))
         return dst
 
 

@@ -410,3 +410,36 @@ def test_rows_of_many_heads_and_blocks():
     a, b = T.pair(2, [300], "Z", 1)
     _run(a, b, 9, n_q=64)
     _run(a, b, 9, n_q=64, window=40, sinks=2, length=290)
+
+
+@pytest.mark.parametrize("lat", ["E8", "D4", "A2", "Z"])
+@pytest.mark.parametrize("dither", [0, 1])
+@pytest.mark.parametrize("k,dk", [(0, 0), (1, 0), (2, 1), (9, 3)])
+def test_every_stream_form_of_many_rows(lat, dither, k, dk):
+    a, b = T.pair(2, [33, 64, 1, 1, 40], lat, k, dither, dk)
+    _run(a, b, 6, n_q=5, dither=dither)
+
+
+def test_first_positions_dropped():
+    """A cache that starts at position 37: sinks and windows that reach before it see nothing there."""
+    hq = _hq()
+    a, b = T.pair(2, [256, 44], "E8")
+    pair = []
+    for c in (a, b):
+        d = hq.KVCache(2, 400, c.cache.params, bits_per_scalar=32.0, max_appends=8, max_append_tokens=64)
+        pair.append(c.repack(d, [(37, 120), (125, 300)], cuda_stream=torch.cuda.current_stream()))
+    held = lambda t: 37 <= t < 120 or t >= 125  # noqa: E731
+    for group, n_q in ((2, 3), (10, 3)):
+        for window, sinks, length in ((0, 0, 300), (50, 40, 300), (50, 4, 140), (20, 10, 37), (20, 10, 30), (400, 4, 300)):
+            _run(*pair, group, n_q=n_q, window=window, sinks=sinks, length=length, held=held)
+
+
+def test_repack_on_a_stream_given_by_its_handle():
+    hq = _hq()
+    a, b = T.pair(1, [64], "E8")
+    side = torch.cuda.Stream()
+    d = hq.KVCache(1, 100, a.cache.params, bits_per_scalar=32.0, max_appends=8, max_append_tokens=64)
+    torch.cuda.synchronize()
+    a.repack(d, cuda_stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(T.vectors(d), T.vectors(a))
