@@ -13,7 +13,9 @@ namespace hq {
 namespace {
 
 constexpr int kCombineWarps = 8;
-constexpr int kCombineSpread = 512;   // rows of all heads up to which a CTA's warps share one row
+// Rows of all heads up to which a CTA's warps share one row (32 rows: 16 us with a warp each, 6 so; 2048 rows, a
+// whole call: 325 and 339 us).
+constexpr int kCombineSpread = 512;
 
 // A query row: the splits' sums rescaled to a common maximum and added, turned back (D H_128, or Q^T),
 // the visible drafts added, divided by the sum of all weights.  Bound by the latency of its loads (a few
