@@ -287,7 +287,6 @@ int attend(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *sp, c
     a.n_q = sp->n_q;
     a.rows = sp->n_q * sp->group;
     a.row_pad = attn_row_pad(a.rows);
-    a.scale = sp->scale;
     a.scale_log2 = (float)((double)sp->scale * 1.4426950408889634074);
     a.q = (const uint16_t *)d_q;
     a.q_ld_tok = q_ld_token;

@@ -67,7 +67,6 @@ struct AttnArgs {
     int out_fp32;
     int64_t out_ld_tok, out_ld_head;
     float *lse;
-    float scale;
 };
 
 cudaError_t launch_attention(int lattice, int dither, const AttnArgs &a, cudaStream_t s);
@@ -703,19 +702,21 @@ struct Source {
 struct Planes {
     uint32_t nc, nr, nu, nsym;
     bool ok, staged;
-    template <int LAT, int FORM>
-    __device__ __forceinline__ void init(const Source &s, const Piece &p) {
-        const uint32_t nt = (uint32_t)p.n;
-        nsym = nt * kTile;
-        nc = (LAT == HQ_E8) ? (16u * nt + 31u) / 32u : 0u;
-        nr = FORM == kFormUnary ? 0u : (nt * tile_rem_bits<Lattice<LAT>::N>(s.k, s.kl) + 31u) >> 5;
-        ok = p.on && p.ok && p.w0 <= p.w1 && p.w1 <= s.cap;
-        const unsigned long long nw = ok ? p.w1 - p.w0 : 0ull;
-        ok = ok && nw >= (unsigned long long)(nc + nr) && (nw - nc - nr) < (unsigned long long)(kMaxUnaryBits / 32u);
-        nu = ok ? (uint32_t)(nw - nc - nr) : 0u;
-        staged = nw <= (unsigned long long)kAttnStage;
-    }
 };
+template <int LAT, int FORM>
+__device__ __forceinline__ Planes planes_of(const Source &s, const Piece &p) {
+    Planes r;
+    const uint32_t nt = (uint32_t)p.n;
+    r.nsym = nt * kTile;
+    r.nc = (LAT == HQ_E8) ? (16u * nt + 31u) / 32u : 0u;
+    r.nr = FORM == kFormUnary ? 0u : (nt * tile_rem_bits<Lattice<LAT>::N>(s.k, s.kl) + 31u) >> 5;
+    r.ok = p.on && p.ok && p.w0 <= p.w1 && p.w1 <= s.cap;
+    const unsigned long long nw = r.ok ? p.w1 - p.w0 : 0ull;
+    r.ok = r.ok && nw >= (unsigned long long)(r.nc + r.nr) && (nw - r.nc - r.nr) < (unsigned long long)(kMaxUnaryBits / 32u);
+    r.nu = r.ok ? (uint32_t)(nw - r.nc - r.nr) : 0u;
+    r.staged = nw <= (unsigned long long)kAttnStage;
+    return r;
+}
 // Whether every query sees every token of a whole chunk.
 __device__ __forceinline__ bool all_see(const AttnArgs &a, const Piece &p, const int64_t *span) {
     const int64_t tl = p.t0 + 31;
@@ -825,8 +826,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
         src.stage(next, sm.stage[warp][buf ^ 1], lane, 32);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
-        Planes pl;
-        pl.template init<LAT, FORM>(src, cur);
+        const Planes pl = planes_of<LAT, FORM>(src, cur);
         const bool staged = pl.staged;
         const uint32_t *const st = sm.stage[warp][buf], *const gsrc = src.words + cur.w0;
         uint32_t *const seg = sm.seg[warp];
@@ -1185,8 +1185,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         // the chunk's words come from both of its warps
         asm volatile("bar.sync %0, 64;" ::"r"(1 + chunk_slot) : "memory");
-        Planes pl;
-        pl.template init<LAT, FORM>(src, cur);
+        const Planes pl = planes_of<LAT, FORM>(src, cur);
         const bool staged = pl.staged;
         const uint32_t *const st = sm.stage[chunk_slot][buf], *const gsrc = src.words + cur.w0;
         uint32_t *const seg = sm.seg[warp];
