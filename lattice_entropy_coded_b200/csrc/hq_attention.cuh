@@ -16,7 +16,11 @@
 //  * z / 64 in fp16: exact for codes up to 2048 without dither, else rounded by at most 2^-11
 //    of its value, and finite over the codec's whole range (|z| < 2^21 + 2 < 64 * 65504);
 //  * the rotated queries as the sum of two fp16 (scaled by a power of two per row): 2^-22;
-//  * the weights p in fp16: 2^-11 of their value (2^-25 of the row's largest below 2^-14).
+//  * the weights w = p e in fp16, e V's scale: it goes into the weights' exponent (log2 p + log2 e), so the
+//    row's running maximum is that of p e, and tokens whose scales lie far apart keep their bits whichever of
+//    them a row sees.  Held as up to 2^15 times the row's largest: 2^-11 of their value, or 2^-36 of the
+//    largest where they are below 2^-25 of it (a long cache's many small weights beside one large, as of a
+//    sink).  The softmax's sum adds w / e in fp32.
 // In attention_kernel a lane of the Rice decoder holds 32 consecutive coordinates of one token; a step of
 // 16 contracted coordinates (mma.sync m16n8k16) takes 4 from each of the 4 lanes of a token, and the queries
 // are laid out in the same order, so K goes from the decoder's registers into the product as it is.
@@ -62,7 +66,7 @@ struct AttnArgs {
     const uint16_t *kd, *vd;
     int64_t d_ld_tok, d_ld_head;
     float *part;                    // [split][head][row_pad][128]
-    float2 *ml;                     // [split][head][row_pad]: maximum (of log2 weights), sum
+    float2 *ml;                     // [split][head][row_pad]: log2 of the unit of both sums, the softmax's sum
     void *out;
     int out_fp32;
     int64_t out_ld_tok, out_ld_head;
@@ -99,6 +103,7 @@ namespace {
 
 constexpr int kTop = 128;   // rows of the append table sampled into shared memory
 constexpr float kNegInf = -INFINITY;
+constexpr float kTopBits = 15.0f;   // the largest weight in fp16 (up to 65504): 2^15
 
 __device__ __forceinline__ uint32_t h2_pack(float a, float b) {
     __half2 h = __floats2half2_rn(a, b);
@@ -509,7 +514,7 @@ struct AttnSmem {
     float xs[kAttnWarps][128];
     uint64_t range[3];
     int64_t span[2];                            // first and last position of the CTA's queries
-    float ev[4], estep;                         // V's scales of the step's chunks (times 64), and the largest
+    float2 ev[4];                               // V's scales of the step's chunks: vscale
     TopRow top[kTop];
 };
 
@@ -616,16 +621,11 @@ __device__ __forceinline__ void load_query(const AttnArgs &a, int head, int row,
 #pragma unroll
     for (int j = 0; j < 4; j++) u[j] = __fmul_rn(u[j], down);
 }
-// The largest of V's scales among the appends of visible chunks [v0, v1), over a warp (each warp takes its
-// share of the appends; the caller joins them): V is summed in its units.
-__device__ __forceinline__ float reference_scale(const AttnArgs &a, const Table<kTop> &tab, uint64_t ia, uint64_t ib, uint64_t v0, uint64_t v1) {
-    float e = 0.0f;
-    if (v0 >= v1) return e;
-    const uint64_t lo = tab.append_of(v0 < ia ? v0 : v0 - ia + ib), hi = tab.append_of(v1 - 1 < ia ? v1 - 1 : v1 - 1 - ia + ib);
-    for (uint64_t i = lo + threadIdx.x; i <= hi; i += blockDim.x) e = fmaxf(e, a.table[1][i].scale_inv);
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, m));
-    return e;
+// What V's scale e of a chunk's append does to its weights: (log2 of 64 e, 1 / (64 e)), codes being in units of
+// 64.  The first is added to the scores, the second takes it out of the softmax's sum again.
+__device__ __forceinline__ float2 vscale(float e) {
+    const float x = __fmul_rn(e, 64.0f);
+    return make_float2(log2f(x), __fdiv_rn(1.0f, x));
 }
 
 // The cache that a warp decodes: K (0) or V (1).
@@ -837,10 +837,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
         else
             ok = scan_segments(gsrc + pl.nc + pl.nr, pl.nu, pl.nsym, seg0, seg1, seg, lane) && ok;
         const int r0 = RW == 4 ? 0 : wi;
-        // codes in units of 64; the appends' scales go into the scores and, relative to the step's largest,
-        // into the weights
+        // codes in units of 64; K's scales go into the scores, V's into the weights
         const float ek = cur.on ? __fmul_rn(cur.e, 64.0f) : 0.0f;
-        if (which && r0 == 0 && lane == 0) sm.ev[ci] = ek;
+        if (which && r0 == 0 && lane == 0) sm.ev[ci] = cur.on ? vscale(cur.e) : make_float2(0.0f, 1.0f);
         const bool open = all_see(a, cur, sm.span);
         bool bad = cur.on && !ok;
 #pragma unroll 1
@@ -915,28 +914,26 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
                 const float2 y = *reinterpret_cast<const float2 *>(sc);
                 x[0] = y.x; x[1] = y.y;
             }
-            float es = sm.ev[0];
-#pragma unroll
-            for (int i = 1; i < RW; i++) es = fmaxf(es, sm.ev[i]);
-            const float ratio = es > 0.0f ? __fdiv_rn(sm.ev[PT * j / 32], es) : 0.0f;
+            const float2 e = sm.ev[PT * j / 32];   // a thread's tokens are of one chunk
             float m = m_run;
 #pragma unroll
-            for (int i = 0; i < PT; i++) m = fmaxf(m, x[i]);
+            for (int i = 0; i < PT; i++) {
+                x[i] = __fadd_rn(x[i], e.x);
+                m = fmaxf(m, x[i]);
+            }
 #pragma unroll
             for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float base = m == kNegInf ? 0.0f : m;   // a row that has seen nothing yet: weights exp2(-inf) = 0
-            const float f = ex2(__fsub_rn(m_run, base));
+            const float top = m == kNegInf ? 0.0f : m;   // a row that has seen nothing yet: weights exp2(-inf) = 0
+            const float f = ex2(__fsub_rn(m_run, top)), base = __fsub_rn(top, kTopBits);
             m_run = m;
             if (j == 0) sm.rescale[r] = f;
-            if (threadIdx.x == 0) sm.estep = es;
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < PT; i++) {
                 x[i] = ex2(__fsub_rn(x[i], base));
                 sum = __fadd_rn(sum, x[i]);
-                x[i] = __fmul_rn(x[i], ratio);
             }
-            l_run = __fmaf_rn(l_run, f, sum);
+            l_run = __fmaf_rn(l_run, f, __fmul_rn(sum, e.y));
             if constexpr (PT == 8)
                 *reinterpret_cast<uint4 *>(sm.p + r * (NT / 2) + 4 * (j ^ (r & 7))) =
                     make_uint4(h2_pack(x[0], x[1]), h2_pack(x[2], x[3]), h2_pack(x[4], x[5]), h2_pack(x[6], x[7]));
@@ -958,14 +955,13 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
                 mma16816(o[0], av, bp[0], bp[1]);
                 mma16816(o[1], av, bp[2], bp[3]);
             }
-            const float es = sm.estep;
 #pragma unroll
             for (int n = 0; n < 2; n++) {
                 const float f0 = sm.rescale[8 * n + 2 * t4], f1 = sm.rescale[8 * n + 2 * t4 + 1];
-                acc[n][0] = __fmaf_rn(acc[n][0], f0, __fmul_rn(o[n][0], es));
-                acc[n][1] = __fmaf_rn(acc[n][1], f1, __fmul_rn(o[n][1], es));
-                acc[n][2] = __fmaf_rn(acc[n][2], f0, __fmul_rn(o[n][2], es));
-                acc[n][3] = __fmaf_rn(acc[n][3], f1, __fmul_rn(o[n][3], es));
+                acc[n][0] = __fmaf_rn(acc[n][0], f0, o[n][0]);
+                acc[n][1] = __fmaf_rn(acc[n][1], f1, o[n][1]);
+                acc[n][2] = __fmaf_rn(acc[n][2], f0, o[n][2]);
+                acc[n][3] = __fmaf_rn(acc[n][3], f1, o[n][3]);
             }
         }
         __syncthreads();   // V, the scores and the weights may be written again
@@ -988,7 +984,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
         float l = l_run;
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, o));
-        if ((threadIdx.x & 15) == 0) a.ml[pbase + (threadIdx.x >> 4)] = make_float2(m_run, l);
+        if ((threadIdx.x & 15) == 0) a.ml[pbase + (threadIdx.x >> 4)] = make_float2(__fsub_rn(m_run, kTopBits), l);
     }
     status = __reduce_or_sync(0xffffffffu, status);
     if (lane == 0 && status) atomicOr(&a.stats[which]->status, status);
@@ -1006,12 +1002,12 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
 //     contracted token in steps of 128 bytes).
 // TMEM: O of both blocks (256 columns), S / P (128), Q's lower part (2 x 64): all 512.
 // Softmax: a thread holds 32 tokens (one chunk) of one row; four threads share a row and exchange their
-// maxima through shared memory.  A row's maximum is moved only when a new one is 2^8 larger, so O is
-// hardly ever rescaled; weights then reach 2^8, still far inside fp16.
+// maxima through shared memory.  A row's maximum is moved only when a new one is 2^4 larger, so O is
+// hardly ever rescaled; weights stand at 2^11 of the row's largest and reach 2^15 before that.
 constexpr int kWideThreads = 512;
 constexpr int kWideRows = 256;
 constexpr uint32_t kWaitLimit = 1u << 20;   // polls of 1 us before the kernel gives up (HQ_ST_TIMEOUT)
-constexpr float kLazyMax = 8.0f;
+constexpr float kLazyMax = 4.0f;
 
 struct WideInfo {
     int64_t t0;
@@ -1028,10 +1024,10 @@ struct WideSmem {
     int64_t qpos[kWideRows];
     float mx[4][128];
     WideInfo info[4];
+    float2 ev[4];                               // vscale of the step's chunks
     uint64_t bar[2];                            // S is there; O is there
     uint64_t range[3];
     int64_t span[2];
-    float eref[16];
     uint32_t sign[4];
     uint32_t tmem;
     TopRow top[kTop];
@@ -1163,11 +1159,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
     const uint64_t nvis = ia + (ie - ib), steps = (nvis + 3) / 4;
     const uint64_t st0 = steps * (uint64_t)split / (uint64_t)a.splits;
     const uint64_t st1 = steps * (uint64_t)(split + 1) / (uint64_t)a.splits;
-    float eref = reference_scale(a, tab, ia, ib, st0 * 4, min(nvis, st1 * 4));
-    if (lane == 0) sm.eref[warp] = eref;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 16; i++) eref = fmaxf(eref, sm.eref[i]);
+    __syncthreads();   // the lower parts have been read: K and V may be written
 
     const int which = warp >> 3, ci = (warp & 7) >> 1, r0 = 2 * (warp & 1), chunk_slot = 4 * which + ci;
     Source src;
@@ -1202,9 +1194,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
             w.ek = cur.on ? __fmul_rn(cur.e, 64.0f) : 0.0f;
             w.open = all_see(a, cur, sm.span);
         }
+        if (which == 1 && r0 == 0 && lane == 0) sm.ev[ci] = cur.on ? vscale(cur.e) : make_float2(0.0f, 1.0f);
         // V's tile is free when the last step's sums are done
         if (which == 1 && step > st0) dead |= !bar_wait(&sm.bar[1], (uint32_t)(step - st0 - 1) & 1u);
-        const float zs = which && cur.on ? __fmul_rn(__fdiv_rn(cur.e, eref), 0.015625f) : 0.015625f;
         uint4 *const tile = which ? sm.v : sm.k;
         bool bad = cur.on && !ok;
 #pragma unroll 1
@@ -1217,7 +1209,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
             const unsigned long long e0 = (unsigned long long)(((cur.t0 + ti) * a.heads + head) * kTile);
             // a tile that did not decode counts as zeros, as a read stores it
             const unsigned lost = decode_round<LAT, DITHER, FORM>(
-                ok, staged, st, gsrc, pl, src, seg, 32u * (uint32_t)(r0 + rr) + lane, valid, e0, zs, sm.pairs,
+                ok, staged, st, gsrc, pl, src, seg, 32u * (uint32_t)(r0 + rr) + lane, valid, e0, 0.015625f, sm.pairs,
                 [&](int g, const uint32_t (&w)[4]) {
                     dst[(4 * (t4 & 1) + g) ^ (tok & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
                 });
@@ -1250,6 +1242,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
             issue_s(0);
         }
         const WideInfo info = sm.info[grp];
+        const float2 ev = sm.ev[grp];
         for (int b = 0; b < nb; b++) {
             dead |= !bar_wait(&sm.bar[0], s_count & 1u);
             s_count++;
@@ -1262,7 +1255,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
                 tmem_ld32(raw, tmS + 32u * grp + lane_base);
                 const float qs = __fmul_rn(sm.qscale[r], info.ek);
 #pragma unroll
-                for (int i = 0; i < 32; i++) x[i] = __fmul_rn(__uint_as_float(raw[i]), qs);
+                for (int i = 0; i < 32; i++) x[i] = __fmaf_rn(__uint_as_float(raw[i]), qs, ev.x);
                 if (!info.open) {
                     const int64_t pos = sm.qpos[r];
 #pragma unroll
@@ -1299,7 +1292,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
                     for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__fmul_rn(__uint_as_float(o[i]), f));
                     tmem_st32(tm + 128u * b + 32u * grp + lane_base, o);
                 }
-                const float base = m == kNegInf ? 0.0f : m;
+                const float base = m == kNegInf ? 0.0f : __fsub_rn(m, kTopBits - kLazyMax);
                 uint32_t pw[16];
                 float sum = 0.0f;
 #pragma unroll
@@ -1308,7 +1301,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
                     sum = __fadd_rn(sum, __fadd_rn(p0, p1));
                     pw[i] = h2_pack(p0, p1);
                 }
-                l = __fmaf_rn(l, f, sum);
+                l = __fmaf_rn(l, f, __fmul_rn(sum, ev.y));
                 m_run[b ? 1 : 0] = m;
                 l_run[b ? 1 : 0] = l;
                 tmem_st16(tmS + 16u * grp + lane_base, pw);
@@ -1338,7 +1331,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 
     // ---- the split's partial results
-    const float eo = __fmul_rn(eref, 64.0f);
     for (int b = 0; b < nb; b++) {
         const bool live = 128 * b + (warp & 3) * 32 < rows;
         const int64_t at = ((int64_t)split * a.heads + head) * a.row_pad + row0 + 128 * b + row;
@@ -1348,13 +1340,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
             float4 *dst = reinterpret_cast<float4 *>(a.part + at * kTile + 32 * grp);
 #pragma unroll
             for (int i = 0; i < 8; i++)
-                dst[i] = make_float4(__fmul_rn(__uint_as_float(o[4 * i]), eo), __fmul_rn(__uint_as_float(o[4 * i + 1]), eo),
-                                     __fmul_rn(__uint_as_float(o[4 * i + 2]), eo), __fmul_rn(__uint_as_float(o[4 * i + 3]), eo));
+                dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                                     __uint_as_float(o[4 * i + 3]));
             sm.mx[grp][row] = b ? l_run[1] : l_run[0];
         }
         __syncthreads();
         if (live && grp == 0)
-            a.ml[at] = make_float2(b ? m_run[1] : m_run[0],
+            a.ml[at] = make_float2(__fsub_rn(b ? m_run[1] : m_run[0], kTopBits - kLazyMax),
                                    __fadd_rn(__fadd_rn(sm.mx[0][row], sm.mx[1][row]), __fadd_rn(sm.mx[2][row], sm.mx[3][row])));
         __syncthreads();
     }
