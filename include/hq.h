@@ -538,10 +538,11 @@ typedef struct hq_rope_spec {
 /* For each token t and each head of q and of k, the bf16 vector x of 128 gives
  *   y = norm ? x / sqrt(mean x^2 + eps) * w : x,
  *   pair i (a, b) of y -> (a cos f - b sin f, b cos f + a sin f),  f = pos[t] * inv_freq[i],
- * in fp32 (the angle's fraction of a turn in fp64), rounded to bf16 once.
+ * in fp32 (the angle's fraction of a turn in fp64), rounded to bf16 once.  An infinity or NaN in x
+ * reaches what the formula makes of it; coordinates past rot_dim pass as y has them.
  *   q, k      : device, bf16, 16-byte aligned; vector (t, h) at [t * ld_token + h * ld_head];
  *               strides % 8 == 0.  heads_q or heads_k may be 0 (its pointers are not used).
- *   d_wq, d_wk: device, bf16 [128], 16-byte aligned, or NULL (ones); not used without norm.
+ *   d_wq, d_wk: device, bf16 [128], 16-byte aligned, or NULL (ones); finite; not used without norm.
  *   d_inv_freq: device, fp64 [rot_dim / 2]: radians per position (theta^(-2 i / rot_dim), or
  *               any scaled form).
  *   d_pos     : device, int64 [tokens], or NULL: pos[t] = pos0 + t.
