@@ -611,7 +611,8 @@ class KVCache:
 
     def repack(self, dst: "KVCache", ranges=None, cuda_stream=None) -> "KVCache":
         """dst's contents become the tokens of `ranges` of this cache (default: all of them, one range), in
-        full chunks; dst: another KVCache of the same heads and params."""
+        full chunks; dst: another KVCache of the same heads and params (KVCache(heads, n, src.cache.params)), which
+        then holds src's rotation too."""
         ranges = ([(0, self.tokens)] if self.tokens else []) if ranges is None else ranges
         need = hq_kv_repack_workspace_bytes(self.heads, ranges)
         # a workspace of the stream that uses it: its memory is free there before the call and after it
@@ -620,6 +621,8 @@ class KVCache:
         with torch.cuda.stream(stream):
             ws = torch.empty(need, dtype=torch.uint8, device=dst.words.device)
         hq_kv_repack(self.cache, dst.cache, ranges, ws, cuda_stream)
+        if self.rotation is not None:   # the one rotation of both: dst may be all that is left to hold it
+            dst.rotation = self.rotation
         return dst
 
 
