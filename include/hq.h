@@ -473,7 +473,7 @@ HQ_API int hq_kv_attention_workspace_bytes(int32_t heads, const hq_attn_spec *sp
  *   d_q       : device, bf16, 16-byte aligned: query token i, head h (of heads * group) at
  *               d_q[i * q_ld_token + h * q_ld_head], 128 elements; strides % 8 == 0.
  *   out       : device, 16-byte aligned, bf16 (out_dtype 0) or fp32 (1), laid out by its
- *               strides (% 8 for bf16, % 4 for fp32, >= 128 between vectors).
+ *               strides (% 8 for bf16, % 4 for fp32); no two vectors share an element.
  *   d_lse     : device, fp32 [n_q, heads * group], or NULL: log of the sum of exp(score) over
  *               the visible tokens (-infinity if none), to merge with attention over others.
  *   workspace : >= hq_kv_attention_workspace_bytes, 16-byte aligned; its contents need no
@@ -546,8 +546,8 @@ typedef struct hq_rope_spec {
  *   d_inv_freq: device, fp64 [rot_dim / 2]: radians per position (theta^(-2 i / rot_dim), or
  *               any scaled form).
  *   d_pos     : device, int64 [tokens], or NULL: pos[t] = pos0 + t.
- *   q_out, k_out: device, bf16, 16-byte aligned, with strides of their own (% 8 == 0, >= 128
- *               between vectors): keys as [heads, tokens, 128] go to hq_kv_append as they are.
+ *   q_out, k_out: device, bf16, 16-byte aligned, with strides of their own (% 8 == 0; no two
+ *               vectors share an element): keys as [heads, tokens, 128] go to hq_kv_append as they are.
  *               Each may be its input itself (same pointer and strides).
  * Asynchronous on cuda_stream; HQ_EINVAL for a bad pointer, stride or spec. */
 HQ_API int hq_qk_norm_rope(const void *q, int64_t q_ld_token, int64_t q_ld_head, int32_t heads_q, const void *k,

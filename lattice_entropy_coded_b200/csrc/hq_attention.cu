@@ -254,8 +254,7 @@ int attend(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *sp, c
     if (!d_q || !aligned(d_q, 16) || q_ld_token < 0 || q_ld_token % 8 || q_ld_head < 0 || q_ld_head % 8) return HQ_EINVAL;
     if (!out || !aligned(out, 16) || out_ld_token < 0 || out_ld_token % m || out_ld_head < 0 || out_ld_head % m)
         return HQ_EINVAL;
-    // no two rows of the output share an element
-    if ((n_heads > 1 && out_ld_head < kTile) || (sp->n_q > 1 && out_ld_token < kTile)) return HQ_EINVAL;
+    if (!vectors_apart(sp->n_q, out_ld_token, n_heads, out_ld_head)) return HQ_EINVAL;
     if (d_lse && !aligned(d_lse, 4)) return HQ_EINVAL;
     if (tree && (!d_kd || !aligned(d_kd, 16) || !d_vd || !aligned(d_vd, 16) || d_ld_token < 0 || d_ld_token % 8 ||
                  d_ld_head < 0 || d_ld_head % 8 || !d_mask || !aligned(d_mask, 8)))

@@ -165,6 +165,22 @@ float scale_fwd(float alpha);                  // fp32(alpha / sqrt(128))
 void set_scratch(EncodeArgs &a, void *ws, uint64_t nch);   // look-back, ticket, done, stats pointers
 uint32_t spin_limit();                         // look-back polls (hq_debug_set_spin_limit)
 
+// Whether no two of n0 x n1 vectors of 128 elements, the one of (i, j) at i * ld0 + j * ld1, share an element:
+// |i ld0 - j ld1| >= 128 for all distances 0 < i < n0, 0 < j < n1, and each stride >= 128 where its dimension
+// has two.
+inline bool vectors_apart(int64_t n0, int64_t ld0, int64_t n1, int64_t ld1) {
+    if ((n0 > 1 && ld0 < kTile) || (n1 > 1 && ld1 < kTile)) return false;
+    if (n0 <= 1 || n1 <= 1) return true;
+    typedef __int128 wide;
+    if ((wide)ld1 >= (wide)(n0 - 1) * ld0 + kTile || (wide)ld0 >= (wide)(n1 - 1) * ld1 + kTile) return true;   // nested
+    if (n0 > n1) return vectors_apart(n1, ld1, n0, ld0);
+    for (int64_t i = 1; i < n0; i++) {
+        const wide at = (wide)i * ld0, j = at / ld1, past = at - j * ld1;   // between j and j + 1
+        if ((j >= 1 && j < n1 && past < kTile) || (j + 1 < n1 && ld1 - past < kTile)) return false;
+    }
+    return true;
+}
+
 // Encoder form: 0 = by size (one CTA for a few chunks, then wide, then grouped, for
 // launches of fewer chunks than the per-warp form has resident warps, per-warp otherwise), 1 =
 // per-warp, 2 = grouped (4 warps per chunk), 3 = wide (16 warps per chunk, 16 lanes
