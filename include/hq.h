@@ -85,7 +85,7 @@ enum hq_lattice { HQ_Z = 0, HQ_A2 = 1, HQ_D4 = 2, HQ_E8 = 3 };
                                were not written; stats.stream_words holds the size needed */
 #define HQ_ST_CORRUPT 0x2u  /* a chunk failed a consistency check while decoding (offsets out of range
                                or not monotone, wrong number of unary terminators); its tiles are zero */
-#define HQ_ST_TIMEOUT 0x4u  /* the chunk-offset look-back gave up after its spin limit */
+#define HQ_ST_TIMEOUT 0x4u  /* a wait (look-back, tensor cores) gave up after its spin limit */
 #define HQ_ST_RANGE 0x8u    /* a scaled coordinate was at or beyond 2^21 in magnitude (or not finite):
                                codes of that call are outside the supported range and unspecified */
 
@@ -581,7 +581,8 @@ HQ_API int hq_device_check(void);
  * predecessor that has not published before it gives up and sets
  * HQ_ST_TIMEOUT (0 restores the default, 2^22).  Process-wide; affects calls
  * made after it.  A timed-out call's stream is unspecified but every write
- * stays inside [0, cap_words). */
+ * stays inside [0, cap_words).  hq_kv_attention and hq_kv_tree_attention of
+ * more than 16 rows a KV head take it for their waits on the tensor cores. */
 HQ_API void hq_debug_set_spin_limit(uint32_t polls);
 
 /* Testing aid: which form of the quantize kernel runs.  0 (default) chooses by

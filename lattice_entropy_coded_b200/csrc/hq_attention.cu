@@ -297,6 +297,7 @@ int attend(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *sp, c
         a.d_ld_tok = d_ld_token;
         a.d_ld_head = d_ld_head;
     }
+    a.wait_limit = spin_limit() < kAttnWaitPolls ? spin_limit() : kAttnWaitPolls;
     a.out = out;
     a.out_fp32 = out_dtype;
     a.out_ld_tok = out_ld_token;

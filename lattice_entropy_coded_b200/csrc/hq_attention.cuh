@@ -44,6 +44,7 @@ constexpr int kAttnMaxGroup = 64;
 constexpr int kAttnWarps = 8;
 constexpr int kAttnStage = 704;                // staged words of a chunk (5.5 bits per scalar)
 constexpr int kAttnCtas = 2 * 148;             // resident CTAs the splits aim at
+constexpr uint32_t kAttnWaitPolls = 1u << 20;  // polls of 1 us for the tensor cores before giving up
 
 struct AttnArgs {
     const uint32_t *words[2];       // K, V
@@ -59,6 +60,7 @@ struct AttnArgs {
     int heads, group, n_q, rows;    // rows = n_q * group query rows per KV head
     int splits, row_pad;            // row_pad: rows of a head in `part`
     int short_steps;                // a step is one chunk (RW = 1), not four
+    uint32_t wait_limit;            // kAttnWaitPolls, or what a test lowered it to
     float scale_log2;               // scale * log2(e)
     const uint16_t *q;
     int64_t q_ld_tok, q_ld_head;
@@ -1006,7 +1008,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
 // hardly ever rescaled; weights stand at 2^11 of the row's largest and reach 2^15 before that.
 constexpr int kWideThreads = 512;
 constexpr int kWideRows = 256;
-constexpr uint32_t kWaitLimit = 1u << 20;   // polls of 1 us before the kernel gives up (HQ_ST_TIMEOUT)
 constexpr float kLazyMax = 4.0f;
 
 struct WideInfo {
@@ -1025,7 +1026,7 @@ struct WideSmem {
     float mx[4][128];
     WideInfo info[4];
     float2 ev[4];                               // vscale of the step's chunks
-    uint64_t bar[2];                            // S is there; O is there
+    uint64_t bar[3];                            // S is there; O is there; all that was issued is done
     uint64_t range[3];
     int64_t span[2];
     uint32_t sign[4];
@@ -1034,10 +1035,14 @@ struct WideSmem {
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
+// The first poll does not wait, each other up to 1 us.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, uint32_t polls) {
     const uint32_t a = smem_u32(bar);
-    for (uint32_t i = 0; i < kWaitLimit; i++) {
-        uint32_t done;
+    uint32_t done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done) : "r"(a), "r"(parity) : "memory");
+    if (done) return true;
+    for (uint32_t i = 1; i < polls; i++) {
         asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
                      : "=r"(done) : "r"(a), "r"(parity), "r"(1000u) : "memory");
         if (done) return true;
@@ -1104,7 +1109,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
 
     if (threadIdx.x == 0) {
         query_span(a, row0, rows, sm.span);
-        for (int i = 0; i < 2; i++)
+        for (int i = 0; i < 3; i++)
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&sm.bar[i])) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -1196,7 +1201,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
         }
         if (which == 1 && r0 == 0 && lane == 0) sm.ev[ci] = cur.on ? vscale(cur.e) : make_float2(0.0f, 1.0f);
         // V's tile is free when the last step's sums are done
-        if (which == 1 && step > st0) dead |= !bar_wait(&sm.bar[1], (uint32_t)(step - st0 - 1) & 1u);
+        if (which == 1 && step > st0) dead |= !bar_wait(&sm.bar[1], (uint32_t)(step - st0 - 1) & 1u, a.wait_limit);
         uint4 *const tile = which ? sm.v : sm.k;
         bool bad = cur.on && !ok;
 #pragma unroll 1
@@ -1244,7 +1249,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
         const WideInfo info = sm.info[grp];
         const float2 ev = sm.ev[grp];
         for (int b = 0; b < nb; b++) {
-            dead |= !bar_wait(&sm.bar[0], s_count & 1u);
+            dead |= !bar_wait(&sm.bar[0], s_count & 1u, a.wait_limit);
             s_count++;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const bool live = 128 * b + (warp & 3) * 32 < rows;   // rows past the last are left out
@@ -1284,7 +1289,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
                 }
                 if (__any_sync(0xffffffffu, f != 1.0f) && step > st0) {
                     // the sums of the last step are there: its barrier has been passed or is passed here
-                    dead |= !bar_wait(&sm.bar[1], (uint32_t)(step - st0 - 1) & 1u);
+                    dead |= !bar_wait(&sm.bar[1], (uint32_t)(step - st0 - 1) & 1u, a.wait_limit);
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     uint32_t o[32];
                     tmem_ld32(o, tm + 128u * b + 32u * grp + lane_base);
@@ -1326,8 +1331,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
         next = after;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (st0 < st1 && !dead) dead = !bar_wait(&sm.bar[1], (uint32_t)(st1 - st0 - 1) & 1u);
+    if (st0 < st1 && !dead) dead = !bar_wait(&sm.bar[1], (uint32_t)(st1 - st0 - 1) & 1u, a.wait_limit);
     dead = __syncthreads_or(dead);
+    if (dead) {
+        // given up: products that are still in flight read this CTA's shared memory and write its TMEM (the wait
+        // for them is never the lowered one)
+        if (threadIdx.x == 0) {
+            umma_commit(&sm.bar[2]);
+            bar_wait(&sm.bar[2], 0u, kAttnWaitPolls);
+        }
+        __syncthreads();
+    }
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 
     // ---- the split's partial results
