@@ -306,17 +306,9 @@ int attend(const hq_kv_cache *k, const hq_kv_cache *v, const hq_attn_spec *sp, c
     cudaStream_t s = (cudaStream_t)cuda_stream;
     const bool cached = sp->len > 0 && k->chunks > 0;
     if (cached) {
-        // chunks a head's queries may see, as far as the host knows: all, or those of the window and the sinks
-        // (one more at each end of either)
-        uint64_t per_head = k->chunks / (uint64_t)k->heads;
-        if (a.window > 0) {
-            const uint64_t w = (uint64_t)(a.window + sp->n_q + a.sinks) + 4;
-            // at the cache's average of tokens to a chunk (only the split depends on it)
-            const uint64_t c = (uint64_t)((double)w * (double)per_head / (double)k->tokens) + 2;
-            if (c < per_head) per_head = c;
-        }
-        a.splits = attn_splits(a.heads, a.rows, per_head);
-        a.short_steps = attn_short(a.heads, a.rows, per_head);
+        const ChunkCount see = visible_chunks(*k, a.window, a.window + sp->n_q + a.sinks);
+        a.short_steps = attn_short(a.heads, a.rows, see.likely);
+        a.splits = attn_splits(a.heads, a.rows, see.most, a.short_steps);
         a.part = (float *)workspace;
         a.ml = (float2 *)(a.part + (size_t)a.splits * a.heads * a.row_pad * kTile);
         if (launch_attention(k->params.lattice, k->params.dither, a, s) != cudaSuccess) return HQ_ECUDA;
@@ -349,7 +341,7 @@ int hq_kv_attention_workspace_bytes(int32_t heads, const hq_attn_spec *spec, siz
     if (!bytes || heads <= 0) return HQ_EINVAL;
     const int rows = spec->n_q * spec->group;
     // as many splits as any cache of this many heads may take
-    const size_t splits = (size_t)attn_splits(heads, rows, UINT64_C(1) << 40);
+    const size_t splits = (size_t)attn_splits(heads, rows, UINT64_C(1) << 40, false);
     *bytes = (splits * (size_t)heads * (size_t)attn_row_pad(rows) * (kTile * sizeof(float) + sizeof(float2)) + 255) &
              ~(size_t)255;
     return HQ_OK;

@@ -93,10 +93,10 @@ inline bool attn_short(int heads, int rows, uint64_t chunks_per_head) {
     return rows <= kNarrowRows && (uint64_t)heads * chunks_per_head <= 2 * (uint64_t)kAttnCtas;
 }
 // Splits of the tokens: the CTAs of all heads and row blocks together fill the GPU once.
-inline int attn_splits(int heads, int rows, uint64_t chunks_per_head) {
+inline int attn_splits(int heads, int rows, uint64_t chunks_per_head, bool short_steps) {
     const int64_t base = rows <= kNarrowRows ? heads : (int64_t)heads * ((rows + 255) / 256);
     int64_t s = (rows <= kNarrowRows ? kAttnCtas : kAttnCtas / 2) / base;
-    const int64_t steps = (int64_t)(attn_short(heads, rows, chunks_per_head) ? chunks_per_head : (chunks_per_head + 3) / 4);
+    const int64_t steps = (int64_t)(short_steps ? chunks_per_head : (chunks_per_head + 3) / 4);
     if (s > steps) s = steps;
     return (int)(s < 1 ? 1 : s);
 }

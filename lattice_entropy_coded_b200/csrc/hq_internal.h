@@ -181,6 +181,31 @@ inline bool vectors_apart(int64_t n0, int64_t ld0, int64_t n1, int64_t ld1) {
     return true;
 }
 
+// Chunks of a head that `span` positions of a window and the sinks reach (all without a window), as far as the host
+// knows; only the split of the work depends on it.
+struct ChunkCount {
+    uint64_t most, likely;
+};
+// At most: where no position is missing, chunks beyond one to 32 tokens may all lie in the window (tokens appended one
+// by one); where some are (hq_kv_repack: fewer chunks than the positions fill), a chunk holds a token.  Likely: the
+// cache's average of chunks to a position, but no fewer than full chunks.  The splits are for the most, so that they
+// never leave the GPU idle (a split too many costs a CTA that ends at once); steps of one chunk, which many chunks
+// make slow, and four where few would be, are chosen by the likely one.
+// One query of 32 heads on 8, E8 at 2 bits, us (the average for both: in brackets): 131072 positions of which sinks and
+// the window's 4096 were kept 34 (117), sinks and 512 kept and 200 appended singly since 55 (546); 32768 tokens and 500
+// appended singly, window 512, 115 (162); 32800 in appends of 100, window 512, 19 (23; 35 with the most for both); full
+// chunks, windows of 64 and 512 as before (15, 17).
+inline ChunkCount visible_chunks(const hq_kv_cache &c, int64_t window, int64_t span) {
+    const uint64_t all = c.chunks / (uint64_t)c.heads, full = (uint64_t)c.tokens / 32, s = (uint64_t)span;
+    if (window <= 0) return {all, all};
+    const uint64_t dense = s / 32 + 4;
+    uint64_t most = s + 4;
+    if (all >= full && dense + (all - full) < most) most = dense + (all - full);
+    uint64_t likely = (uint64_t)((double)s * (double)all / (double)c.tokens) + 2;
+    if (likely < dense) likely = dense;
+    return {most < all ? most : all, likely < all ? likely : all};
+}
+
 // Encoder form: 0 = by size (one CTA for a few chunks, then wide, then grouped, for
 // launches of fewer chunks than the per-warp form has resident warps, per-warp otherwise), 1 =
 // per-warp, 2 = grouped (4 warps per chunk), 3 = wide (16 warps per chunk, 16 lanes
