@@ -442,13 +442,15 @@ def hq_kv_tree_attention(k: hq_kv_cache, v: hq_kv_cache, spec: hq_attn_spec, q: 
                          vd: torch.Tensor, mask: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
                          lse: torch.Tensor | None = None, cuda_stream=None) -> int:
     """As hq_kv_attention for n_q drafted tokens that are not cached: kd, vd bf16 [heads, n_q, 128] (equal
-    strides, the last 1); mask int64 [n_q], bit j of mask[i]: query i sees draft j."""
+    strides where a dimension has two or more, the last 1); mask int64 [n_q], bit j of mask[i]: query i sees draft j."""
     _attn_shapes(k, spec, q, out, lse)
-    assert kd.dtype == vd.dtype == torch.bfloat16 and kd.stride() == vd.stride() and kd.stride(2) == 1
-    assert tuple(kd.shape) == tuple(vd.shape) == (k.heads, spec.n_q, 128)
+    assert kd.dtype == vd.dtype == torch.bfloat16 and tuple(kd.shape) == tuple(vd.shape) == (k.heads, spec.n_q, 128)
+    ks, vs = kd.stride(), vd.stride()   # (that of a dimension of one says nothing)
+    assert ks[2] == vs[2] == 1 and (ks == vs or all(n == 1 or i == j for n, i, j in zip(kd.shape, ks, vs)))
+    dh, dt = ks[0] if k.heads > 1 else 128, ks[1] if spec.n_q > 1 else 128
     assert mask.dtype == torch.int64 and mask.is_contiguous() and mask.numel() == spec.n_q
     return _check(_lib.hq_kv_tree_attention(C.byref(k), C.byref(v), C.byref(spec), _ptr(q), q.stride(0), q.stride(1),
-                                            _ptr(kd), _ptr(vd), kd.stride(1), kd.stride(0), _ptr(mask), _ptr(out),
+                                            _ptr(kd), _ptr(vd), dt, dh, _ptr(mask), _ptr(out),
                                             1 if out.dtype == torch.float32 else 0, out.stride(0), out.stride(1),
                                             _ptr(lse), _ptr(workspace), workspace.numel(), _stream(cuda_stream)),
                   "hq_kv_tree_attention")
