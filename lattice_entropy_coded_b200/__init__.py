@@ -457,7 +457,7 @@ def hq_kv_tree_attention(k: hq_kv_cache, v: hq_kv_cache, spec: hq_attn_spec, q: 
 
 
 def _ranges(ranges):
-    flat = [int(x) for r in ranges for x in r]
+    flat = [int(x) for begin, end in ranges for x in (begin, end)]   # (anything but pairs is a ValueError)
     return (C.c_int64 * max(len(flat), 1))(*flat), len(flat) // 2
 
 
@@ -615,7 +615,8 @@ class KVCache:
         """dst's contents become the tokens of `ranges` of this cache (default: all of them, one range), in
         full chunks; dst: another KVCache of the same heads and params (KVCache(heads, n, src.cache.params)), which
         then holds src's rotation too."""
-        ranges = ([(0, self.tokens)] if self.tokens else []) if ranges is None else ranges
+        # a list: an iterator would have nothing left after the workspace's size
+        ranges = ([(0, self.tokens)] if self.tokens else []) if ranges is None else list(ranges)
         need = hq_kv_repack_workspace_bytes(self.heads, ranges)
         # a workspace of the stream that uses it: its memory is free there before the call and after it
         stream = cuda_stream if cuda_stream is None or isinstance(cuda_stream, torch.cuda.Stream) else \
