@@ -548,7 +548,8 @@ typedef struct hq_rope_spec {
  *   d_pos     : device, int64 [tokens], or NULL: pos[t] = pos0 + t.
  *   q_out, k_out: device, bf16, 16-byte aligned, with strides of their own (% 8 == 0; no two
  *               vectors share an element): keys as [heads, tokens, 128] go to hq_kv_append as they are.
- *               Each may be its input itself (same pointer and strides).
+ *               Each may be its input itself (same pointer and strides; HQ_EINVAL under other
+ *               strides), and shares no element with an input otherwise.
  * Asynchronous on cuda_stream; HQ_EINVAL for a bad pointer, stride or spec. */
 HQ_API int hq_qk_norm_rope(const void *q, int64_t q_ld_token, int64_t q_ld_head, int32_t heads_q, const void *k,
                            int64_t k_ld_token, int64_t k_ld_head, int32_t heads_k, int64_t tokens,

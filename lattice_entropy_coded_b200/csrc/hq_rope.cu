@@ -254,7 +254,10 @@ int check_side(const void *x, int64_t ld_tok, int64_t ld_head, const void *w, vo
     if (!x || !y || !aligned(x, 16) || !aligned(y, 16) || !aligned(w, 16)) return HQ_EINVAL;
     if (ld_tok < 0 || ld_tok % 8 || ld_head < 0 || ld_head % 8) return HQ_EINVAL;
     if (out_tok < 0 || out_tok % 8 || out_head < 0 || out_head % 8) return HQ_EINVAL;
-    return vectors_apart(tokens, out_tok, heads, out_head) ? HQ_OK : HQ_EINVAL;
+    if (!vectors_apart(tokens, out_tok, heads, out_head)) return HQ_EINVAL;
+    // in place only vector by vector: under other strides one half-warp would write what another has yet to read
+    if (x == y && ((tokens > 1 && ld_tok != out_tok) || (heads > 1 && ld_head != out_head))) return HQ_EINVAL;
+    return HQ_OK;
 }
 
 }  // namespace

@@ -61,6 +61,26 @@ def test_norm_rope_refuses_vectors_that_overlap(side, t, h):
     assert A._rope(**bad) == A._hq().HQ_EINVAL
 
 
+@pytest.mark.parametrize("bad", [dict(qo=A.P, qot=2048), dict(qo=A.P, qot=128, qoh=1024), dict(ko=2 * A.P),
+                                 dict(ko=2 * A.P, kot=256, koh=1280)], ids=str)
+def test_norm_rope_refuses_to_work_in_place_under_other_strides(bad):
+    """The inputs lie at strides (1024, 128) and (256, 128)."""
+    assert A._rope(**bad) == A._hq().HQ_EINVAL
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens,heads", [(1, 4), (5, 1)])
+def test_norm_rope_in_place_where_a_stride_says_nothing(tokens, heads):
+    hq = A._hq()
+    x = torch.randn(tokens, heads, 128, device="cuda").to(torch.bfloat16)
+    f = 10000.0 ** (-torch.arange(64, dtype=torch.float64, device="cuda") / 64)
+    want = torch.empty_like(x)
+    hq.hq_qk_norm_rope(x, None, hq.rope_spec(), f, want, None)
+    other = x.as_strided(x.shape, (x.stride(0), 1024, 1) if heads == 1 else (4096, 128, 1))
+    hq.hq_qk_norm_rope(x, None, hq.rope_spec(), f, other, None)
+    assert torch.equal(x, want)
+
+
 @pytest.mark.gpu
 def test_vectors_that_lie_between_one_another():
     """Strides 640 and 256: the second token's vectors lie between the first's, none on another."""
