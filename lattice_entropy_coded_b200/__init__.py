@@ -632,12 +632,21 @@ class KVCache:
 class KVAttention:
     """Attention over the K and V caches of one layer.  Owns the workspace, which serves calls that follow one
     another (calls on several streams at once need an object each); its size covers every number of queries, so it
-    never moves under a captured graph."""
+    never moves under a captured graph.  Keep the object while such a graph may run."""
 
     def __init__(self, k: KVCache, v: KVCache, group: int, scale: float = 128 ** -0.5, window: int = 0, sinks: int = 0):
         self.k, self.v, self.group, self.scale, self.window, self.sinks = k, v, group, scale, window, sinks
         need = max(hq_kv_attention_workspace_bytes(k.heads, attn_spec(0, scale, n, group)) for n in range(1, 65))
         self.workspace = torch.empty(need, dtype=torch.uint8, device=k.words.device)
+        self._streams = {_stream(None)}   # that the workspace's memory is known to be used on
+
+    def _use(self, cuda_stream) -> int | None:
+        """The call's stream, on which the workspace's memory is not given to others before the call is done."""
+        s = _stream(cuda_stream)
+        if s not in self._streams:
+            self.workspace.record_stream(torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream())
+            self._streams.add(s)
+        return s
 
     def _spec(self, n_q: int, length: int | None) -> hq_attn_spec:
         return attn_spec(self.k.tokens if length is None else length, self.scale, n_q, self.group, self.window,
@@ -647,12 +656,13 @@ class KVAttention:
                  cuda_stream=None) -> torch.Tensor:
         """q, out [n_q, heads * group, 128]: the last n_q cached tokens' attention."""
         spec = self._spec(q.shape[0], length)
-        hq_kv_attention(self.k.cache, self.v.cache, spec, q, out, self.workspace, lse, cuda_stream)
+        hq_kv_attention(self.k.cache, self.v.cache, spec, q, out, self.workspace, lse, self._use(cuda_stream))
         return out
 
     def tree(self, q: torch.Tensor, kd: torch.Tensor, vd: torch.Tensor, mask: torch.Tensor, out: torch.Tensor,
              length: int | None = None, lse: torch.Tensor | None = None, cuda_stream=None) -> torch.Tensor:
         """The attention of n_q drafted tokens over the cache and one another (hq_kv_tree_attention)."""
         spec = self._spec(q.shape[0], length)
-        hq_kv_tree_attention(self.k.cache, self.v.cache, spec, q, kd, vd, mask, out, self.workspace, lse, cuda_stream)
+        hq_kv_tree_attention(self.k.cache, self.v.cache, spec, q, kd, vd, mask, out, self.workspace, lse,
+                             self._use(cuda_stream))
         return out
