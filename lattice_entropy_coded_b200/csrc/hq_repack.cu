@@ -92,8 +92,8 @@ __device__ __forceinline__ NewChunk new_chunk(const RepackArgs &a, uint64_t c) {
 }
 
 // First unary bit of every tile of a chunk of n tiles (start[0 .. n]) by the whole warp; false unless
-// the plane of nu words holds exactly 128 n terminators.  64 words at a time, as the attention's scan:
-// population counts, two sets of 32 scanned in one register; a word that holds the last terminator of a
+// the plane of nu words holds exactly 128 n terminators.  128 words at a time, as the attention's scan:
+// population counts, two sets of 32 scanned in one register (twice); a word that holds the last terminator of a
 // tile (at most one) notes itself, and each lane then finds its tile's bit.
 __device__ __forceinline__ bool tile_starts(const uint32_t *un, uint32_t nu, uint32_t n, uint32_t *start, int lane) {
     uint32_t seen = 0;
