@@ -446,9 +446,9 @@ HQ_API int hq_kv_scores(const hq_kv_cache *cache, const void *d_q, int32_t group
  * being the reconstructions of hq_kv_read before their rounding to bf16.  A row that sees
  * nothing gives zeros.  Scores, maxima, sums and the output's sums are fp32; codes enter the
  * products in fp16 (at most 2^-11 of their value off, or 2^-19; codes up to 2048 without dither
- * exact), queries as two fp16, and each weight times its token's scale of V (1 / alpha, whose
- * spread over a cache is free between 2^-100 and 2^100) in fp16 too: at most 2^-11 of its value
- * off, or 2^-36 of the row's largest. */
+ * exact), queries as two fp16, and each weight times its token's scale of V (1 / alpha; alphas of
+ * one cache within a factor of 2^100) in fp16 too: at most 2^-11 of its value off, or 2^-36 of the
+ * row's largest. */
 typedef struct hq_attn_spec {
     int64_t len;    /* cached tokens to use: positions [0, len), len <= tokens of both caches */
     int64_t window; /* positions a query sees back, its own included; 0: all */

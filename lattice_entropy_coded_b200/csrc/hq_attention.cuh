@@ -27,7 +27,7 @@
 //
 // Bound: the decoder's integer work, not bytes nor products: 38 lane-instructions a code with dither (E8, 2
 // bits), at 3.4 of 4 issued a cycle. One query over 8 x 32768 tokens at 2 bits: 174 us (104 of them the
-// decode's at that rate); 64 drafts: 292 us.
+// decode's at that rate); 64 drafts: 299 us.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -82,8 +82,8 @@ cudaError_t launch_attention_d4(int dither, const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_attention_e8(int dither, const AttnArgs &a, cudaStream_t s);
 
 // Query rows of one CTA: one block of 16 (attention_kernel), or up to 256 in blocks of 128 (attention_wide).
-// Over 8 heads, E8 at 2 bits: 16 rows of 32768 tokens take 175 us by the first, 231 by the second; 20 rows 354
-// (two blocks, so every token twice) and 231; of 4099 tokens 36 and 45, 58 and 46.
+// Over 8 heads, E8 at 2 bits: 16 rows of 32768 tokens take 170 us by the first, about 224 by the second; 20 rows
+// 354 (two blocks, so every token twice) and 224; of 4099 tokens 35 and 43, 58 and 43.
 constexpr int kNarrowRows = 16;
 inline int attn_row_pad(int rows) { return rows <= kNarrowRows ? 16 : (rows + 127) / 128 * 128; }
 // Whether steps are of one chunk, whose rounds four warps share, instead of a chunk to a warp: while

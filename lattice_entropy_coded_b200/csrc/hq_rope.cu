@@ -13,7 +13,7 @@
 // 4 pairs, so the rotation needs no exchange and the norm four shuffles.  A half-warp keeps
 // its token's 4 angles and the side's 8 weights and walks over heads, so the sines cost one
 // evaluation per token and lane; short calls spread a token's heads over more half-warps instead.
-// 8191 tokens of 32 + 8 heads: 34 us, 4.9 TB/s (75 % of a copy).  Four CTAs to an SM at 64 registers (by events on
+// 8191 tokens of 32 + 8 heads: 35 us, 4.8 TB/s (74 % of a copy).  Four CTAs to an SM at 64 registers (by events on
 // a cold L2: three 51 us, four 47, five 62); 8 pairs to a lane instead of 4 60 us, the next heads' loads ahead of
 // this one's arithmetic 47 to 68 us, the fast sines no difference.
 #include <cuda_bf16.h>
