@@ -445,7 +445,7 @@ HQ_API int hq_kv_scores(const hq_kv_cache *cache, const void *d_q, int32_t group
  * over the visible tokens t the cache holds (hq_kv_repack may have dropped some), K and V
  * being the reconstructions of hq_kv_read before their rounding to bf16.  A row that sees
  * nothing gives zeros.  Scores, maxima, sums and the output's sums are fp32; codes enter the
- * products in fp16 (at most 2^-11 of their value off, or 2^-19; codes up to 2048 without dither
+ * products in fp16 (at most 2^-11 of their value off, or 2^-17; codes up to 2048 without dither
  * exact), queries as two fp16, and each weight times its token's scale of V (1 / alpha; alphas of
  * one cache within a factor of 2^100) in fp16 too: at most 2^-11 of its value off, or 2^-36 of the
  * row's largest. */

@@ -13,8 +13,9 @@
 // back, adds the drafted tokens of a tree (whose K and V are plain bf16) and writes the output.
 //
 // The products run on the tensor cores in fp16 with fp32 sums:
-//  * z / 64 in fp16: exact for codes up to 2048 without dither, else rounded by at most 2^-11
-//    of its value, and finite over the codec's whole range (|z| < 2^21 + 2 < 64 * 65504);
+//  * z / 256 in fp16: exact for codes up to 2048 without dither, else rounded by at most 2^-11 of its value (or
+//    2^-17), and finite over the codec's whole range (symbols below 2^22, so |z| < 2^23 + 4 < 256 * 65504: E8's last
+//    code of a block is 4 m + 2 p + c, with |m| up to 2^21);
 //  * the rotated queries as the sum of two fp16 (scaled by a power of two per row): 2^-22;
 //  * the weights w = p e in fp16, e V's scale: it goes into the weights' exponent (log2 p + log2 e), so the
 //    row's running maximum is that of p e, and tokens whose scales lie far apart keep their bits whichever of
@@ -105,6 +106,7 @@ namespace {
 
 constexpr int kTop = 128;   // rows of the append table sampled into shared memory
 constexpr float kNegInf = -INFINITY;
+constexpr float kCodeUnit = 256.0f;  // of the codes in fp16
 constexpr float kTopBits = 15.0f;   // the largest weight in fp16 (up to 65504): 2^15
 
 __device__ __forceinline__ uint32_t h2_pack(float a, float b) {
@@ -623,10 +625,10 @@ __device__ __forceinline__ void load_query(const AttnArgs &a, int head, int row,
 #pragma unroll
     for (int j = 0; j < 4; j++) u[j] = __fmul_rn(u[j], down);
 }
-// What V's scale e of a chunk's append does to its weights: (log2 of 64 e, 1 / (64 e)), codes being in units of
-// 64.  The first is added to the scores, the second takes it out of the softmax's sum again.
+// What V's scale e of a chunk's append does to its weights: (log2 of 256 e, 1 / (256 e)), codes being in units of
+// 256.  The first is added to the scores, the second takes it out of the softmax's sum again.
 __device__ __forceinline__ float2 vscale(float e) {
-    const float x = __fmul_rn(e, 64.0f);
+    const float x = __fmul_rn(e, kCodeUnit);
     return make_float2(log2f(x), __fdiv_rn(1.0f, x));
 }
 
@@ -839,8 +841,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
         else
             ok = scan_segments(gsrc + pl.nc + pl.nr, pl.nu, pl.nsym, seg0, seg1, seg, lane) && ok;
         const int r0 = RW == 4 ? 0 : wi;
-        // codes in units of 64; K's scales go into the scores, V's into the weights
-        const float ek = cur.on ? __fmul_rn(cur.e, 64.0f) : 0.0f;
+        // codes in units of 256; K's scales go into the scores, V's into the weights
+        const float ek = cur.on ? __fmul_rn(cur.e, kCodeUnit) : 0.0f;
         if (which && r0 == 0 && lane == 0) sm.ev[ci] = cur.on ? vscale(cur.e) : make_float2(0.0f, 1.0f);
         const bool open = all_see(a, cur, sm.span);
         bool bad = cur.on && !ok;
@@ -853,7 +855,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) attention_kernel(const __g
             const unsigned long long e0 = (unsigned long long)(((cur.t0 + ti) * a.heads + head) * kTile);
             // a tile that did not decode counts as zeros, as a read stores it
             const unsigned lost = decode_round<LAT, DITHER, FORM>(
-                ok, staged, st, gsrc, pl, src, seg, 32u * (uint32_t)(r0 + rr) + lane, valid, e0, 0.015625f, sm.pairs,
+                ok, staged, st, gsrc, pl, src, seg, 32u * (uint32_t)(r0 + rr) + lane, valid, e0, 1.0f / kCodeUnit, sm.pairs,
                 [&](int g, const uint32_t (&x)[4]) {
 #pragma unroll
                     for (int i = 0; i < 4; i++) w[4 * g + i] = x[i];
@@ -1196,7 +1198,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
             WideInfo &w = sm.info[ci];
             w.t0 = cur.t0;
             w.n = cur.on ? cur.n : 0;
-            w.ek = cur.on ? __fmul_rn(cur.e, 64.0f) : 0.0f;
+            w.ek = cur.on ? __fmul_rn(cur.e, kCodeUnit) : 0.0f;
             w.open = all_see(a, cur, sm.span);
         }
         if (which == 1 && r0 == 0 && lane == 0) sm.ev[ci] = cur.on ? vscale(cur.e) : make_float2(0.0f, 1.0f);
@@ -1214,7 +1216,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide(const __grid_c
             const unsigned long long e0 = (unsigned long long)(((cur.t0 + ti) * a.heads + head) * kTile);
             // a tile that did not decode counts as zeros, as a read stores it
             const unsigned lost = decode_round<LAT, DITHER, FORM>(
-                ok, staged, st, gsrc, pl, src, seg, 32u * (uint32_t)(r0 + rr) + lane, valid, e0, 0.015625f, sm.pairs,
+                ok, staged, st, gsrc, pl, src, seg, 32u * (uint32_t)(r0 + rr) + lane, valid, e0, 1.0f / kCodeUnit, sm.pairs,
                 [&](int g, const uint32_t (&w)[4]) {
                     dst[(4 * (t4 & 1) + g) ^ (tok & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
                 });

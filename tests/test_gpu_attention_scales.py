@@ -33,7 +33,7 @@ def _cache(heads, parts, lat, seed, dither, k=0):
 def _check(out, lse, q, ck, cv, e, keep, group):
     """kvtest.tolerance (roundings relative to each visible token's share), and what fp16 adds at its lower end:
     weights times scales below 2^-25 of the row's largest are off by up to 2^-36 of it (they stand at 2^11 of that or
-    more, and fp16's last place is 2^-24), codes by up to 2^-19 a coordinate (z / 64 in steps of 2^-24)."""
+    more, and fp16's last place is 2^-24), codes by up to 2^-17 a coordinate (half of z / 256's steps of 2^-24)."""
     k, v = T.vectors(ck), T.vectors(cv)
     heads = k.shape[0]
     vis = keep.any(0)
@@ -42,7 +42,7 @@ def _check(out, lse, q, ck, cv, e, keep, group):
     s = torch.einsum("nhgd,htd->nhgt", q.double().unflatten(1, (heads, group)), k) * SCALE
     w = torch.softmax(s.masked_fill(~keep[:, None, None], -math.inf), -1)
     z = torch.where(keep[:, None], v.norm(dim=-1) / e, 0.0)             # [n_q, heads, tokens]: codes a row sees
-    low = 2.0 ** -36 * (w * e).amax(-1) * z.sum(-1)[..., None] + 2.0 ** -19 * math.sqrt(128) * (w * e).sum(-1)
+    low = 2.0 ** -36 * (w * e).amax(-1) * z.sum(-1)[..., None] + 2.0 ** -17 * math.sqrt(128) * (w * e).sum(-1)
     lim = tol + low.flatten(1, 2) + 2.0 ** -24 * ref.norm(dim=-1)
     err = (out.double() - ref).norm(dim=-1)
     assert torch.isfinite(out).all()
