@@ -28,7 +28,7 @@
 //
 // Bound: the decoder's integer work, not bytes nor products: 38 lane-instructions a code with dither (E8, 2
 // bits), at 3.4 of 4 issued a cycle. One query over 8 x 32768 tokens at 2 bits: 174 us (104 of them the
-// decode's at that rate); 64 drafts: 299 us.
+// decode's at that rate); 64 drafts: 297 us.
 #pragma once
 
 #include <cuda_fp16.h>
